@@ -320,6 +320,80 @@ MLA_API mla_status mla_sparse_prefill(const void* q, int s_q, int h_q, int d_qk,
                                       void* stream);
 
 /*
+ * Appending new tokens to the paged cache.  One pass over a step's new tokens: the latent is
+ * normalised (optionally), the position columns of keys and queries are rotated, and each token's
+ * row goes to the cache row that its slot names.
+ *
+ * For token t with latent x [512], key position columns e [64] and position n:
+ *   y    = norm_weight ? x * rsqrt(mean(x^2) + norm_eps) * norm_weight : x        (float32)
+ *   R(n) = rotation of pair i by the angle whose cosine and sine are cos_sin[n][i] and
+ *          cos_sin[n][32 + i]:  (a, b) -> (a cos - b sin, b cos + a sin); pair i is columns
+ *          (2 i, 2 i + 1) when interleaved, else (i, i + 32)                       (float32)
+ *   16-bit cache:  row slots[t] = [ y | R(n) e ], each rounded once to the cache's type
+ *   MLA_BF16_FP8KV: row slots[t] = e4m3(y_i / s_k), s_k, bf16(R(n) e), where for k = 0..3
+ *          s_k = max(max_{i in block k} |y_i| * (1/448), 2^-126) in float32 (block k: latent columns
+ *          [128 k, 128 k + 128)) and the quotient is rounded to float32, then to the nearest e4m3
+ *          value.  y is quantized from float32: it is not rounded to bfloat16 before.
+ *   queries (q_pe not null):  q[t][h][512:576] = R(n) q_pe[t][h], rounded once; other columns of q
+ *          are left as they were.  q_pe may be those columns of q themselves.
+ *
+ *   latent         device [num_tokens] rows of 512, latent_stride values apart
+ *   k_pe           device [num_tokens] rows of 64, k_pe_stride values apart; null with d_qk 512
+ *   norm_weight    device [512] or null;  norm_eps >= 0
+ *   positions      device int32 [num_tokens] (not read with d_qk 512)
+ *   cos_sin        device float32 [max_position, 64]
+ *   slots          device int32 [num_tokens]: flat cache rows (page * 64 + offset).  A negative slot
+ *                  is padding: no row is written (the token's query columns are rotated all the
+ *                  same).  Slots of one call are distinct; of two tokens with one slot the row
+ *                  holds parts of either.
+ *   kvcache        device [num_blocks, 64, 1, d_qk] or [num_blocks, 64, 1, 656] bytes; d_qk 576, or
+ *                  512 (16-bit only: rows without position columns, no queries)
+ *   q_pe, q        device; element (t, h, j) at t * token_stride + h * head_stride + j; both or
+ *                  neither null; rows of q (576 wide) must not overlap
+ *   dtype          type of latent, k_pe, norm_weight, q_pe, q and a 16-bit cache (bfloat16 for
+ *                  MLA_BF16_FP8KV)
+ *   device_status  device int32 or null: a slot outside the cache or a position outside the table
+ *                  leaves the token's row (and for a position its query columns) as it was and
+ *                  records MLA_ERR_DEVICE_CHECK there if it holds 0
+ * Every pointer but positions and slots is 16-byte aligned and every stride a multiple of 8 values,
+ * at least 0.  Enqueues one kernel on `stream`.
+ */
+MLA_API mla_status mla_append_kvcache(const void* latent, long long latent_stride, const void* k_pe,
+                                      long long k_pe_stride, const void* norm_weight, float norm_eps,
+                                      const int32_t* positions, const float* cos_sin, int max_position,
+                                      const int32_t* slots, int num_tokens, void* kvcache, int num_blocks, int page_size,
+                                      int h_kv, int d_qk, int dtype, int interleaved, const void* q_pe,
+                                      long long q_pe_token_stride, long long q_pe_head_stride, void* q,
+                                      long long q_token_stride, long long q_head_stride, int h_q, int32_t* device_status,
+                                      void* stream);
+
+/*
+ * Page keys: one 8-bit summary per cache page, which page selection scores.
+ *
+ * For every page j of request b with prev_seqlens[b] / 64 <= j < cache_seqlens[b] / 64 (whole
+ * divisions: the pages that the tokens between the two lengths completed; a page that is not full
+ * has no key), with rows r_0 .. r_63 at physical page P = block_table[b][j]:
+ *   m              = (r_0 + ... + r_63) / 64          (right to the last bit of float32, whatever the
+ *                                                      order: the sum is kept to about 48 bits)
+ *   page_scales[P] = max(max_i |m_i| * (1/127), 2^-126)                     (float32)
+ *   page_keys[P]   = m_i / page_scales[P], rounded to float32 and then to the nearest whole number
+ * An FP8 cache's latents are bf16(e4m3 * scale), as for attention.  Other pages' keys are left as
+ * they were.  A page with infinities or NaN gets an unspecified key.
+ *
+ *   kvcache, dtype, d_qk   as for mla_append_kvcache
+ *   block_table    device int32 [batch, max_blocks_per_seq]
+ *   prev_seqlens, cache_seqlens   device int32 [batch]
+ *   page_keys      device int8 [num_blocks, d_qk], 16-byte aligned;  page_scales float32 [num_blocks]
+ *   device_status  device int32 or null: an entry outside the cache (skipped), or a length beyond the
+ *                  table (its pages past the table are skipped), records MLA_ERR_DEVICE_CHECK
+ * Enqueues one kernel on `stream`.
+ */
+MLA_API mla_status mla_summarize_pages(const void* kvcache, int num_blocks, int page_size, int h_kv, int d_qk, int dtype,
+                                       const int32_t* block_table, int max_blocks_per_seq, const int32_t* prev_seqlens,
+                                       const int32_t* cache_seqlens, int batch, int8_t* page_keys, float* page_scales,
+                                       int32_t* device_status, void* stream);
+
+/*
  * Reads the device status word of a workspace (synchronises `stream`).
  * *device_status receives MLA_OK or the first device-side error recorded by a
  * decode call that used this workspace; clear != 0 then zeroes the workspace's

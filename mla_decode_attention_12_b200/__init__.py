@@ -7,14 +7,20 @@ Public calls (the names of the pages' API; "FlashMLA" usage page, deepep.org):
   (``indices=``: the token-level sparse decode);
 * :func:`flash_mla_sparse_fwd` -- the sparse MLA prefill, returns ``(out, max_logits, lse)``.
 
-Both are thin wrappers over the C ABI in ``include/mla_decode.h``; the kernels
+Around the decode:
+
+* :func:`mla_append_kvcache` -- new tokens' rows into the cache (norm, rotation, quantization);
+* :func:`mla_summarize_pages` -- 8-bit page keys of completed pages.
+
+All are thin wrappers over the C ABI in ``include/mla_decode.h``; the kernels
 live in ``csrc/``.  ``workloads`` generates seeded synthetic inputs.
 """
 from .api import (DecodeCall, flash_mla_sparse_fwd, flash_mla_with_kvcache, get_mla_metadata, get_mla_metadata_host,
                   get_mla_metadata_sparse_host, metadata_sizes, num_sm_parts, read_device_status, workspace_bytes,
                   workspace_zero_bytes)
+from .cache import mla_append_kvcache, mla_summarize_pages
 from ._lib import MLAError
 
 __all__ = ["DecodeCall", "flash_mla_sparse_fwd", "flash_mla_with_kvcache", "get_mla_metadata", "get_mla_metadata_host",
-           "get_mla_metadata_sparse_host", "metadata_sizes", "num_sm_parts", "read_device_status", "workspace_bytes",
-           "workspace_zero_bytes", "MLAError"]
+           "get_mla_metadata_sparse_host", "metadata_sizes", "mla_append_kvcache", "mla_summarize_pages",
+           "num_sm_parts", "read_device_status", "workspace_bytes", "workspace_zero_bytes", "MLAError"]

@@ -26,6 +26,7 @@ STATUS_NAMES = {
 
 # Every entry point the header declares, with its ctypes signature.
 _I, _P, _SZ, _F = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "mla_status_string": ([_I], ctypes.c_char_p),
     "mla_num_sm_parts": ([_I, ctypes.POINTER(_I)], _I),
@@ -60,6 +61,14 @@ SIGNATURES = {
                             _P, _I, _I, _I, _F,              # indices, topk, dv, dtype, sm_scale
                             _P, _I, _P,                      # tile_md, num_parts, num_splits
                             _P, _P, _P, _P, _SZ, _P], _I),   # out, max_logits, lse, workspace, bytes, stream
+    "mla_append_kvcache": ([_P, _LL, _P, _LL, _P, _F,        # latent, stride, k_pe, stride, norm_weight, norm_eps
+                            _P, _P, _I, _P, _I,              # positions, cos_sin, max_position, slots, num_tokens
+                            _P, _I, _I, _I, _I, _I, _I,      # kvcache, num_blocks, page_size, h_kv, d_qk, dtype, interleaved
+                            _P, _LL, _LL, _P, _LL, _LL, _I,  # q_pe, strides, q, strides, h_q
+                            _P, _P], _I),                    # device_status, stream
+    "mla_summarize_pages": ([_P, _I, _I, _I, _I, _I,         # kvcache, num_blocks, page_size, h_kv, d_qk, dtype
+                             _P, _I, _P, _P, _I,             # block_table, max_blocks, prev_seqlens, seqlens, batch
+                             _P, _P, _P, _P], _I),           # page_keys, page_scales, device_status, stream
 }
 
 _lock = threading.Lock()

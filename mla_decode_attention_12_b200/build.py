@@ -14,8 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "_mla_decode.so")
-SOURCES = [os.path.join(CSRC, "mla_decode.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "scheduler.cuh")] + [
+SOURCES = [os.path.join(CSRC, f) for f in ("mla_decode.cu", "cache_ops.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("host_util.cuh", "ptx.cuh", "scheduler.cuh")] + [
     os.path.join(ROOT, "include", "mla_decode.h")]
 
 NVCC_FLAGS = [

@@ -58,6 +58,7 @@
 #include <vector>
 
 #include "../../include/mla_decode.h"
+#include "host_util.cuh"
 #include "ptx.cuh"
 #include "scheduler.cuh"
 
@@ -1797,29 +1798,6 @@ static void workspace_pointers(void* workspace, int batch, int groups, int num_p
     prm.max_accum = reinterpret_cast<float*>(ws + kControlBytes + small);
     prm.o_accum = reinterpret_cast<float*>(ws + kControlBytes + 2 * small);
 }
-
-// Runs a per-device set-up step (a kernel attribute) once for each device it is used on,
-// from any number of host threads.
-struct PerDeviceOnce {
-    static constexpr int kMaxDevices = 64;
-    std::mutex m;
-    std::atomic<bool> done[kMaxDevices] = {};
-
-    template <typename F>
-    cudaError_t run(F&& setup)
-    {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        if (dev < 0 || dev >= kMaxDevices) return setup();  // outside the table: every call
-        if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-        std::lock_guard<std::mutex> lock(m);
-        if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-        e = setup();
-        if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
-        return e;
-    }
-};
 
 template <bool kRope, bool kFp16, bool kPadHeads, bool kFp8, bool kSparse>
 static cudaError_t launch_splitkv(int grid, cudaStream_t stream, const CUtensorMap* maps, const DecodeParams& prm)
