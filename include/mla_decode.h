@@ -320,6 +320,51 @@ MLA_API mla_status mla_sparse_prefill(const void* q, int s_q, int h_q, int d_qk,
                                       void* stream);
 
 /*
+ * Attention of ragged runs of new tokens over the paged cache: chunks of prompts and decode steps of
+ * any length in one call.  Run b is the query tokens [cu_seqlens_q[b], cu_seqlens_q[b + 1]) of the
+ * call's total_q; its keys are the first L_b = cache_seqlens[b] cached rows of its pages, the run's own
+ * tokens among them (append them first).
+ *
+ * For token i of run b (0 <= i < n_b, n_b its tokens) and head h:
+ *   n    = causal ? clamp(L_b - n_b + 1 + i, 0, L_b) : L_b        (bottom-right mask)
+ *   x_j  = softmax_scale * <q[t,h,:], k_j>  (j < n),  lse = log(sum_j exp(x_j))   (-inf when n = 0)
+ *   o    = sum_j exp(x_j - lse) * k_j[0:512]                                       (0 when n = 0)
+ * Cached rows past the last one that a group of 128 query rows (tokens x heads) sees are not read into its
+ * result, whatever they hold.  Rows of q, o and lse past cu_seqlens_q[batch] are left as they were.
+ *
+ * mla_get_metadata_varlen: the tile scheduler, once per step for every layer.  Each run's rows are cut
+ *   into groups of 128; a group's work is the pages that its last token sees.
+ *   cu_seqlens_q   device int32 [batch + 1], ascending within [0, total_q]
+ *   cache_seqlens  device int32 [batch]
+ *   total_q        query tokens of the call (rows of q); batch <= 16384, total_q * h_q < 2^30
+ *   plan           device int32 [mla_varlen_plan_ints(...)], 16-byte aligned, written (opaque)
+ *   One small kernel on `stream`.  Runs that are not an ascending split of the tokens give a plan
+ *   without work; the decode call with it records MLA_ERR_DEVICE_CHECK and writes nothing.
+ * mla_get_metadata_varlen_host: the same schedule into host memory (8-byte aligned).
+ * mla_decode_varlen:
+ *   q              device [total_q, h_q, d_qk], dtype `dtype`, 16-byte aligned
+ *   kvcache, block_table, dv, dtype, softmax_scale   as for mla_decode_with_kvcache
+ *   plan, num_parts   from mla_get_metadata_varlen for the same batch, total_q and h_q
+ *   o              device [total_q, h_q, 512], 16-byte aligned;  lse device float32 [total_q, h_q]
+ *   workspace      >= mla_decode_varlen_workspace_bytes(num_parts), control block zero as for
+ *                  mla_decode_with_kvcache (one workspace serves both)
+ *   Enqueues the split-KV and the combine kernel on `stream`.
+ */
+MLA_API size_t mla_varlen_plan_ints(int batch, int total_q, int h_q, int h_kv, int num_parts);
+MLA_API mla_status mla_get_metadata_varlen(const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, int batch, int total_q,
+                                           int h_q, int h_kv, int causal, int num_parts, int is_fp8_kvcache, int32_t* plan,
+                                           void* stream);
+MLA_API mla_status mla_get_metadata_varlen_host(const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, int batch,
+                                                int total_q, int h_q, int h_kv, int causal, int num_parts,
+                                                int is_fp8_kvcache, int32_t* plan);
+MLA_API size_t mla_decode_varlen_workspace_bytes(int num_parts);
+MLA_API mla_status mla_decode_varlen(const void* q, int total_q, int h_q, int d_qk, const void* kvcache, int num_blocks,
+                                     int page_size, int h_kv, const int32_t* block_table, int batch,
+                                     int max_blocks_per_seq, int dv, int dtype, const int32_t* plan, int num_parts,
+                                     float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
  * Appending new tokens to the paged cache.  One pass over a step's new tokens: the latent is
  * normalised (optionally), the position columns of keys and queries are rotated, and each token's
  * row goes to the cache row that its slot names.

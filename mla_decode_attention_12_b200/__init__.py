@@ -7,6 +7,9 @@ Public calls (the names of the pages' API; "FlashMLA" usage page, deepep.org):
   (``indices=``: the token-level sparse decode);
 * :func:`flash_mla_sparse_fwd` -- the sparse MLA prefill, returns ``(out, max_logits, lse)``.
 
+* :func:`flash_mla_varlen_with_kvcache` -- ragged runs of new tokens (chunks of prompts beside decode
+  steps) over the paged cache, with :func:`get_mla_metadata_varlen`.
+
 Around the decode:
 
 * :func:`mla_append_kvcache` -- new tokens' rows into the cache (norm, rotation, quantization);
@@ -19,8 +22,12 @@ from .api import (DecodeCall, flash_mla_sparse_fwd, flash_mla_with_kvcache, get_
                   get_mla_metadata_sparse_host, metadata_sizes, num_sm_parts, read_device_status, workspace_bytes,
                   workspace_zero_bytes)
 from .cache import mla_append_kvcache, mla_summarize_pages
+from .varlen import (VarlenPlan, flash_mla_varlen_with_kvcache, get_mla_metadata_varlen, get_mla_metadata_varlen_host,
+                     varlen_workspace_bytes)
 from ._lib import MLAError
 
-__all__ = ["DecodeCall", "flash_mla_sparse_fwd", "flash_mla_with_kvcache", "get_mla_metadata", "get_mla_metadata_host",
-           "get_mla_metadata_sparse_host", "metadata_sizes", "mla_append_kvcache", "mla_summarize_pages",
+__all__ = ["DecodeCall", "VarlenPlan", "flash_mla_sparse_fwd", "flash_mla_varlen_with_kvcache", "flash_mla_with_kvcache",
+           "get_mla_metadata", "get_mla_metadata_host", "get_mla_metadata_sparse_host", "get_mla_metadata_varlen",
+           "get_mla_metadata_varlen_host", "varlen_workspace_bytes",
+           "metadata_sizes", "mla_append_kvcache", "mla_summarize_pages",
            "num_sm_parts", "read_device_status", "workspace_bytes", "workspace_zero_bytes", "MLAError"]

@@ -61,6 +61,15 @@ SIGNATURES = {
                             _P, _I, _I, _I, _F,              # indices, topk, dv, dtype, sm_scale
                             _P, _I, _P,                      # tile_md, num_parts, num_splits
                             _P, _P, _P, _P, _SZ, _P], _I),   # out, max_logits, lse, workspace, bytes, stream
+    "mla_varlen_plan_ints": ([_I, _I, _I, _I, _I], _SZ),
+    "mla_get_metadata_varlen": ([_P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P], _I),
+    "mla_get_metadata_varlen_host": ([_P, _P, _I, _I, _I, _I, _I, _I, _I, _P], _I),
+    "mla_decode_varlen_workspace_bytes": ([_I], _SZ),
+    "mla_decode_varlen": ([_P, _I, _I, _I,              # q, total_q, h_q, d_qk
+                           _P, _I, _I, _I,              # kvcache, num_blocks, page_size, h_kv
+                           _P, _I, _I, _I, _I,          # block_table, batch, max_blocks, dv, dtype
+                           _P, _I, _F,                  # plan, num_parts, scale
+                           _P, _P, _P, _SZ, _P], _I),   # o, lse, workspace, ws_bytes, stream
     "mla_append_kvcache": ([_P, _LL, _P, _LL, _P, _F,        # latent, stride, k_pe, stride, norm_weight, norm_eps
                             _P, _P, _I, _P, _I,              # positions, cos_sin, max_position, slots, num_tokens
                             _P, _I, _I, _I, _I, _I, _I,      # kvcache, num_blocks, page_size, h_kv, d_qk, dtype, interleaved

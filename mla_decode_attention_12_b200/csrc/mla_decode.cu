@@ -202,6 +202,7 @@ struct DecodeParams {
     const int32_t* indices;   // sparse decode: [batch][topk] flat cache rows (page * 64 + offset), -1 invalid
     const int32_t* md;
     const int32_t* num_splits;
+    const int32_t* vgroups;   // ragged runs: [groups][kVarInts] (see scheduler.cuh)
     const void* q;
     const void* kvcache;
     void* o;
@@ -339,15 +340,20 @@ __device__ __forceinline__ int request_len(const int32_t* seqlens, int const_len
 }
 
 // Iterates the chunks (vb, blk_lo, blk_hi) of one scheduler partition.
+template <bool kVarlen>
 struct ChunkIter {
     int vb, blk, end_vb, end_blk, batch;
-    const int32_t* seqlens;
+    const int32_t* seqlens;  // ragged runs: the group table
     int const_len;  // the length of every request when seqlens is null
 
     __device__ bool next(int& out_vb, int& lo, int& hi)
     {
         if (!(vb < end_vb || (vb == end_vb && blk < end_blk))) return false;
-        const int n = pages_of(request_len(seqlens, const_len, vb_request(vb, batch)));
+        int n;
+        if constexpr (kVarlen)
+            n = pages_of(seqlens[kVarInts * vb + kVarLimit]);
+        else
+            n = pages_of(request_len(seqlens, const_len, vb_request(vb, batch)));
         out_vb = vb;
         lo = blk;
         hi = (vb == end_vb) ? end_blk : n;
@@ -356,6 +362,26 @@ struct ChunkIter {
         return true;
     }
 };
+
+// Request of a virtual batch, and the cached rows it may read: all of the request's, or, for a
+// group of a ragged run, those that its last query token sees.
+template <bool kVarlen>
+__device__ __forceinline__ int chunk_request(const DecodeParams& p, int vb)
+{
+    if constexpr (kVarlen)
+        return p.vgroups[kVarInts * vb + kVarReq];
+    else
+        return vb_request(vb, p.batch);
+}
+
+template <bool kVarlen>
+__device__ __forceinline__ int chunk_len(const DecodeParams& p, int vb, int b)
+{
+    if constexpr (kVarlen)
+        return p.vgroups[kVarInts * vb + kVarLimit];
+    else
+        return request_len(p.seqlens, p.topk, b);
+}
 
 __device__ __forceinline__ uint32_t pack2(float a, float b, bool fp16)
 {
@@ -399,12 +425,13 @@ __device__ __forceinline__ int checked_page(const DecodeParams& p, int page)
 //   O   columns [0, 256):  d_v chunk i (256 wide) at [128 i, 128 i + 128)
 //   S   columns [256, 288) and [288, 320): two page buffers
 // Thread t of the softmax warps owns row t % 64 and token / d_v half t / 64.
-template <bool kRope, bool kFp16, bool kPadHeads, bool kFp8 = false, bool kSparse = false>
+template <bool kRope, bool kFp16, bool kPadHeads, bool kFp8 = false, bool kSparse = false, bool kVarlen = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
     mla_splitkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const DecodeParams p)
 {
     static_assert(!kFp8 || (kRope && !kFp16), "the FP8 cache has d_qk = 576 and bfloat16 queries");
+    static_assert(!kVarlen || (!kSparse && !kPadHeads), "ragged runs read a block table and have no padding heads");
     using L = Layout<kRope, kFp8>;
     constexpr int kNumThreads = kFp8 ? kThreadsFp8 : kThreads;
     extern __shared__ uint8_t smem_raw[];
@@ -505,7 +532,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 
     Sync sync{s_bar + kOffAbort, map_to_cta(s_bar + kOffAbort, cta ^ 1u), p.status};
     const int32_t* md = p.md + part * kMdInts;
-    ChunkIter chunks{md[0], md[1], md[2], md[3], p.batch, p.seqlens, p.topk};
+    if constexpr (kVarlen)  // a schedule of runs that do not split the tokens is empty and says why
+        if (blockIdx.x == 0 && threadIdx.x == 0 && md[5] != 0) atomicCAS(p.status, 0, md[5]);
+    ChunkIter<kVarlen> chunks{md[0], md[1], md[2], md[3], p.batch, kVarlen ? p.vgroups : p.seqlens, p.topk};
     const int begin_vb = md[0];
     const int begin_split = md[4];
 
@@ -553,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         int vb, lo, hi;
         while (ok && chunks.next(vb, lo, hi)) {
             if (hi <= lo) continue;
-            const int Lb = request_len(p.seqlens, p.topk, vb_request(vb, p.batch));
+            const int Lb = chunk_len<kVarlen>(p, vb, vb_request(vb, p.batch));
             for (int blk = lo; blk < hi && ok; ++blk, rk.advance(), kring.advance()) {
                 if (!(ok = wwait(bar(kBarRawKFull + rk.stage), rk.phase))) break;
                 if (tl_conv) TL_EV(kEvConvRaw);
@@ -635,8 +664,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                 bool ok = true;
                 while (ok && chunks.next(vb, lo, hi)) {
                     if (hi <= lo) continue;
-                    const int b = vb_request(vb, p.batch), rg = vb_group(vb, p.batch);
-                    const int y = rg * kRowsPerGroup + y_off;
+                    // a request's rows are one slice of the tensor, or (ragged runs) all rows are
+                    const int b = kVarlen ? 0 : vb_request(vb, p.batch);
+                    const int y = (kVarlen ? p.vgroups[kVarInts * vb + kVarRow0] : vb_group(vb, p.batch) * kRowsPerGroup) + y_off;
                     if (!(ok = sync.wait(bar(kBarQFree), (k & 1) ^ 1))) break;
                     TL_EV(kEvQLoad);
                     for (int r = 0; r < 3 && ok; ++r) {
@@ -710,7 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     const uint8_t* kv = static_cast<const uint8_t*>(p.kvcache);
                     while (ok && chunks.next(vb, lo, hi)) {
                         if (hi <= lo) continue;
-                        const int b = vb_request(vb, p.batch);
+                        const int b = chunk_request<kVarlen>(p, vb);
                         const int32_t* table = p.block_table + static_cast<size_t>(b) * p.max_blocks;
                         int entry = table_entry(p, table, lo), entry_next = 0;
                         for (int blk = lo; blk < hi; ++blk, ring.advance(), entry = entry_next) {
@@ -783,7 +813,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 #endif
                 while (ok && chunks.next(vb, lo, hi)) {
                     if (hi <= lo) continue;
-                    const int b = vb_request(vb, p.batch);
+                    const int b = chunk_request<kVarlen>(p, vb);
                     const int32_t* table = p.block_table + static_cast<size_t>(b) * p.max_blocks;
 #ifdef MLA_TEST_WITHHOLD_K_PAGE
                     const int withheld = (part == 0 && first_chunk) ? lo + MLA_TEST_WITHHOLD_K_PAGE : -1;
@@ -937,8 +967,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                 auto wwait = [&](uint32_t b_, uint32_t par) { return __all_sync(0xffffffffu, sync.wait(b_, par)); };
                 while (ok && chunks.next(vb, lo, hi)) {
                     if (hi <= lo) continue;
-                    const int b = vb_request(vb, p.batch);
-                    const int Lb = request_len(p.seqlens, p.topk, b);
+                    const int b = chunk_request<kVarlen>(p, vb);
+                    const int Lb = chunk_len<kVarlen>(p, vb, b);
                     const int tail = Lb % kPage;
                     const int last_page = pages_of(Lb) - 1;
                     const int32_t* table = p.block_table + static_cast<size_t>(b) * p.max_blocks;
@@ -1126,6 +1156,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         const uint32_t o_free_lead = lead_bar(kBarOFree);
         auto wwait = [&](uint32_t b_, uint32_t par) { return __all_sync(0xffffffffu, sync.wait(b_, par)); };
         auto q_row_ptr = [&](int qvb, bool& valid) {
+            if constexpr (kVarlen) {
+                const int32_t* gr = p.vgroups + kVarInts * qvb;
+                const int at = 64 * static_cast<int>(cta) + r;
+                valid = at < gr[kVarRows];
+                return reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
+                                                      static_cast<size_t>(gr[kVarRow0] + at) * p.d_qk * 2);
+            }
             const int qrow_idx = vb_group(qvb, p.batch) * kRowsPerGroup + 64 * static_cast<int>(cta) + r;
             valid = qrow_idx < p.rows;
             return reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
@@ -1153,7 +1190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                 __syncwarp();
                 if (lane == 0) {
                     __threadfence();  // ... and the whole warp's, before the counter update
-                    atomicAdd(p.ctl + 2 * announce_vb, 1);
+                    atomicAdd(p.ctl + 2 * announce_vb, 1);  // (ragged runs: the counter of a partition)
                 }
                 __syncwarp();
                 announce_vb = -1;
@@ -1162,16 +1199,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         if (t == 0) TL_EV(kEvSetupDone);
         bool have = chunks.next(vb, lo, hi);
         while (ok && have) {
-            const int b = vb_request(vb, p.batch), rg = vb_group(vb, p.batch);
-            const int Lb = request_len(p.seqlens, p.topk, b);
-            const int row = rg * kRowsPerGroup + 64 * static_cast<int>(cta) + r;
-            const bool row_valid = row < p.rows;
-            const int s_tok = row / p.h_q;
-            int n_vis = Lb;
-            if (p.causal) n_vis = min(max(Lb - p.s_q + 1 + s_tok, 0), Lb);
-            const int nsplit = p.num_splits[vb + 1] - p.num_splits[vb];
             const int split_idx = (vb == begin_vb) ? begin_split : 0;
-            const size_t slot = static_cast<size_t>(p.num_splits[vb]) + split_idx;  // split partial's workspace slot
+            int b, rg, row, n_vis, nsplit;
+            bool row_valid;
+            size_t slot;  // split partial's workspace slot
+            if constexpr (kVarlen) {
+                // row: of the call's total_q * h_q query rows; what its token sees follows from its place
+                const int32_t* gr = p.vgroups + kVarInts * vb;
+                b = 0;
+                rg = gr[kVarRow0];
+                row = rg + 64 * static_cast<int>(cta) + r;
+                row_valid = row < rg + gr[kVarRows];
+                n_vis = min(max(gr[kVarSeen] + row / p.h_q, 0), gr[kVarLen]);
+                nsplit = gr[kVarSplits];
+                slot = 2 * static_cast<size_t>(part) + (split_idx > 0 ? 0 : 1);
+            } else {
+                b = vb_request(vb, p.batch), rg = vb_group(vb, p.batch);
+                const int Lb = request_len(p.seqlens, p.topk, b);
+                row = rg * kRowsPerGroup + 64 * static_cast<int>(cta) + r;
+                row_valid = row < p.rows;
+                const int s_tok = row / p.h_q;
+                n_vis = Lb;
+                if (p.causal) n_vis = min(max(Lb - p.s_q + 1 + s_tok, 0), Lb);
+                nsplit = p.num_splits[vb + 1] - p.num_splits[vb];
+                slot = static_cast<size_t>(p.num_splits[vb]) + split_idx;
+            }
             const int n = hi - lo;
             float m_ref = -INFINITY, l_half = 0.f;
             float row_max = -INFINITY;  // the chunk's largest scaled logit, base 2 (the prefill's max_logits)
@@ -1192,7 +1244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 
             for (int j = 0; j < n; ++j) {
                 if (j == j_prefetch) {
-                    ChunkIter peek = chunks;
+                    ChunkIter<kVarlen> peek = chunks;
                     int pvb, plo, phi;
                     while (peek.next(pvb, plo, phi))
                         if (phi > plo) {
@@ -1353,8 +1405,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             // skipped.
             {
                 const int row_g = 64 * static_cast<int>(cta) + (t & 32) + lane;  // this lane's row in the group
-                const int grow = rg * kRowsPerGroup + row_g;
-                const bool live = grow < p.rows && (!kPadHeads || grow % p.h_q < p.active_heads);
+                const int grow = kVarlen ? rg + row_g : rg * kRowsPerGroup + row_g;
+                bool live;
+                if constexpr (kVarlen)
+                    live = row_g < p.vgroups[kVarInts * vb + kVarRows];
+                else
+                    live = grow < p.rows && (!kPadHeads || grow % p.h_q < p.active_heads);
                 uint8_t* const o_row = static_cast<uint8_t*>(p.o) + (static_cast<size_t>(b) * p.rows + grow) * (kDv * 2);
                 float* const acc_row = p.o_accum + (slot * kRowsPerGroup + row_g) * static_cast<size_t>(kDv);
 #pragma unroll 1
@@ -1420,7 +1476,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     p.max_accum[slot * kRowsPerGroup + 64 * cta + r] = row_max;
                 }
             }
-            if (nsplit > 1) announce_vb = vb;
+            if constexpr (kVarlen) {
+                // the partition that holds split 1: splits 1, 2, ... lie in consecutive partitions
+                if (nsplit > 1) announce_vb = split_idx > 0 ? part - split_idx + 1 : part + 1;
+            } else {
+                if (nsplit > 1) announce_vb = vb;
+            }
             if (!empty) ++k;
             g += (n > 0 ? n : 0);
             have = have_next;
@@ -1451,8 +1512,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 //  * many splits (few virtual batches, long sequences): one CTA per row, warp w
 //    sums splits w, w + 4, ... and the four partial sums are added through shared
 //    memory, so a row's splits are read four at a time.
-template <bool kFp16, bool kSplitParallel>
-__global__ void __launch_bounds__(128) mla_combine_kernel(DecodeParams p)
+template <bool kFp16, bool kSplitParallel, bool kVarlen>
+__device__ __forceinline__ void combine_rows(const DecodeParams& p)
 {
     // No wait for the whole split-KV grid: the CTAs of a virtual batch start combining once
     // its splits are announced (8 warps per split), while other partitions still run.  This
@@ -1461,10 +1522,25 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(DecodeParams p)
     // combine CTA of the virtual batch past the wait clears both counters for the next call.
     // (The schedule was written by the metadata grid, complete before the split-KV grid
     // allowed this one to launch.)
-    const int vb = blockIdx.x;
-    const int slot0 = p.num_splits[vb];
-    const int nsplit = p.num_splits[vb + 1] - slot0;
-    if (nsplit <= 1) return;
+    // blockIdx.x: the virtual batch, or, for ragged runs, the partition that holds its split 1 (at
+    // most one split virtual batch starts its second split in a partition).
+    int vb = blockIdx.x, slot0, nsplit, rows_here, row0 = 0;
+    if constexpr (kVarlen) {
+        const int32_t* md = p.md + kMdInts * blockIdx.x;
+        if (md[4] != 1) return;
+        const int32_t* gr = p.vgroups + kVarInts * md[0];
+        nsplit = gr[kVarSplits];
+        rows_here = gr[kVarRows];
+        row0 = gr[kVarRow0];
+        slot0 = 2 * (static_cast<int>(blockIdx.x) - 1);
+    } else {
+        slot0 = p.num_splits[vb];
+        nsplit = p.num_splits[vb + 1] - slot0;
+        if (nsplit <= 1) return;
+    }
+    // Workspace slot of split k, relative to slot0.  Ragged runs: a partition has two, one for a
+    // chunk that continues an earlier partition's and one for a chunk that a later one continues.
+    auto slot_of = [](int k) -> size_t { return kVarlen ? (k == 0 ? 1 : 2 * k) : k; };
     __shared__ int go;
     if (threadIdx.x == 0) {
         const int want = 8 * nsplit;
@@ -1491,12 +1567,19 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(DecodeParams p)
     }
     __syncthreads();
     if (!go) return;
-    const int b = vb_request(vb, p.batch), rg = vb_group(vb, p.batch);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = kSplitParallel ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y) * 4 + warp;
-    const int rows_here = min(kRowsPerGroup, p.rows - rg * kRowsPerGroup);
-    // uniform over the CTA in the split-parallel layout; padding heads are not combined
-    if (r >= rows_here || (rg * kRowsPerGroup + r) % p.h_q >= p.active_heads) return;
+    size_t at;  // row of o and lse
+    if constexpr (kVarlen) {
+        if (r >= rows_here) return;
+        at = static_cast<size_t>(row0) + r;
+    } else {
+        const int b = vb_request(vb, p.batch), rg = vb_group(vb, p.batch);
+        rows_here = min(kRowsPerGroup, p.rows - rg * kRowsPerGroup);
+        // uniform over the CTA in the split-parallel layout; padding heads are not combined
+        if (r >= rows_here || (rg * kRowsPerGroup + r) % p.h_q >= p.active_heads) return;
+        at = static_cast<size_t>(b) * p.rows + rg * kRowsPerGroup + r;
+    }
     const float* lse_k = p.lse_accum + static_cast<size_t>(slot0) * kRowsPerGroup + r;
     const float* max_k = p.max_accum + static_cast<size_t>(slot0) * kRowsPerGroup + r;
     // The splits' LSEs (and maxima) are read once, in one round trip: lane i holds splits i,
@@ -1507,14 +1590,14 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(DecodeParams p)
 #pragma unroll
     for (int i = 0; i < kLseRegs; ++i) {
         const int k = lane + 32 * i;
-        lk[i] = k < nsplit ? __ldcg(lse_k + static_cast<size_t>(k) * kRowsPerGroup) : -INFINITY;
-        mk[i] = (p.max_logits && k < nsplit) ? __ldcg(max_k + static_cast<size_t>(k) * kRowsPerGroup) : -INFINITY;
+        lk[i] = k < nsplit ? __ldcg(lse_k + slot_of(k) * kRowsPerGroup) : -INFINITY;
+        mk[i] = (p.max_logits && k < nsplit) ? __ldcg(max_k + slot_of(k) * kRowsPerGroup) : -INFINITY;
     }
     float mx = fmaxf(fmaxf(lk[0], lk[1]), lk[2]);
     float row_max = fmaxf(fmaxf(mk[0], mk[1]), mk[2]);  // the largest base-2 scaled logit (the prefill's max_logits)
     for (int k = lane + 32 * kLseRegs; k < nsplit; k += 32) {
-        mx = fmaxf(mx, __ldcg(lse_k + static_cast<size_t>(k) * kRowsPerGroup));
-        if (p.max_logits) row_max = fmaxf(row_max, __ldcg(max_k + static_cast<size_t>(k) * kRowsPerGroup));
+        mx = fmaxf(mx, __ldcg(lse_k + slot_of(k) * kRowsPerGroup));
+        if (p.max_logits) row_max = fmaxf(row_max, __ldcg(max_k + slot_of(k) * kRowsPerGroup));
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -1525,7 +1608,7 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(DecodeParams p)
     if (mx != -INFINITY) {
 #pragma unroll
         for (int i = 0; i < kLseRegs; ++i) sum += expf(lk[i] - mx);  // exp(-inf) = 0 for absent splits
-        for (int k = lane + 32 * kLseRegs; k < nsplit; k += 32) sum += expf(__ldcg(lse_k + static_cast<size_t>(k) * kRowsPerGroup) - mx);
+        for (int k = lane + 32 * kLseRegs; k < nsplit; k += 32) sum += expf(__ldcg(lse_k + slot_of(k) * kRowsPerGroup) - mx);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -1535,7 +1618,7 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(DecodeParams p)
 #pragma unroll
     for (int i = 0; i < kLseRegs; ++i) wk[i] = expf(lk[i] - lse);
     auto weight = [&](int k) {
-        if (k >= 32 * kLseRegs) return expf(__ldcg(lse_k + static_cast<size_t>(k) * kRowsPerGroup) - lse);
+        if (k >= 32 * kLseRegs) return expf(__ldcg(lse_k + slot_of(k) * kRowsPerGroup) - lse);
         const float w = k < 32 ? wk[0] : (k < 64 ? wk[1] : wk[2]);
         return __shfl_sync(0xffffffffu, w, k & 31);
     };
@@ -1555,7 +1638,7 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(DecodeParams p)
             for (int j = 0; j < 4; ++j) {
                 const int k = k0 + step * j;
                 if (k < nsplit) {
-                    const float4* s4 = src + static_cast<size_t>(k) * stride4;
+                    const float4* s4 = src + slot_of(k) * stride4;
                     v[j][0] = __ldcg(s4);
                     v[j][1] = __ldcg(s4 + 32);
                     v[j][2] = __ldcg(s4 + 64);
@@ -1595,16 +1678,24 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(DecodeParams p)
                 acc[i].x += o.x; acc[i].y += o.y; acc[i].z += o.z; acc[i].w += o.w;
             }
     }
-    const int row = rg * kRowsPerGroup + r;
-    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + (static_cast<size_t>(b) * p.rows + row) * kDv * 2);
+    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + at * kDv * 2);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         dst[lane + 32 * i] = make_uint2(pack2(acc[i].x, acc[i].y, kFp16), pack2(acc[i].z, acc[i].w, kFp16));
     if (lane == 0) {
-        const size_t at = static_cast<size_t>(b) * p.rows + row;
         p.lse[at] = p.lse_base2 ? lse * 1.4426950408889634f : lse;
         if (p.max_logits) p.max_logits[at] = row_max;
     }
+}
+
+template <bool kFp16, bool kSplitParallel, bool kVarlen = false>
+__global__ void __launch_bounds__(128) mla_combine_kernel(const __grid_constant__ DecodeParams p)
+{
+    combine_rows<kFp16, kSplitParallel, kVarlen>(p);
+    // This grid ends after the split-KV grid has: a later grid of the stream that starts early
+    // (programmatic launch) waits for this one alone, and must find the unsplit rows written and
+    // q and the cache read.  One CTA waits for all.
+    if (blockIdx.x == 0 && blockIdx.y == 0) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ metadata kernel
@@ -1704,6 +1795,101 @@ static size_t metadata_smem_bytes(int nv, int num_parts)
     return static_cast<size_t>(nv) * (8 + 4 + 4) + static_cast<size_t>(num_parts) * 8 + 16;
 }
 
+// The schedule of ragged runs: one CTA of kVarThreads threads.  The group table is built in tiles of
+// one group per thread (its run found by binary search in the runs' first groups), with the cost
+// prefix carried from tile to tile; then one thread per partition, as above.  Latency bound: once
+// per step, for every layer.  C: the prefix sums, in shared memory where they fit (a partition's
+// binary searches then take about 0.1 us instead of several), else behind the table.
+// Runs that are not an ascending split of the tokens give an empty schedule whose md rows carry an
+// error (field 5), which the decode records.
+constexpr int kVarThreads = 1024;
+constexpr int kVarMaxRuns = 16384;
+
+__global__ void __launch_bounds__(kVarThreads) mla_metadata_varlen_kernel(const int32_t* cu, const int32_t* seqlens,
+                                                                          int batch, int total_q, int h_q, int causal,
+                                                                          int num_parts, int fixed_cost, int32_t* md,
+                                                                          int32_t* groups, long long* c_global)
+{
+    extern __shared__ __align__(16) uint8_t meta_smem[];
+    grid_launch_dependents();
+    __shared__ long long warp_tot_ll[32];
+    __shared__ int warp_tot_i[32];
+    __shared__ int bad;
+    int32_t* first = reinterpret_cast<int32_t*>(meta_smem);  // [batch + 1] first group of each run
+    int32_t* begins = first + ((batch + 2) & ~1);              // [num_parts][2]
+    long long* C = c_global ? c_global : reinterpret_cast<long long*>(begins + 2 * num_parts);
+    const int tid = threadIdx.x;
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    for (int b = tid; b < batch; b += kVarThreads) {
+        const int t0 = cu[b], t1 = cu[b + 1];
+        const bool fine = t0 >= 0 && t1 >= t0 && t1 <= total_q;
+        if (!fine) bad = 1;
+        first[b] = fine ? row_groups((t1 - t0) * h_q) : 0;
+    }
+    __syncthreads();
+    const bool skip = bad != 0;
+    int nv = 0;
+    block_exclusive_scan(first, batch, warp_tot_i, nv);
+    if (skip) nv = 0;
+    long long total = 0;
+    for (int v0 = 0; v0 < nv; v0 += kVarThreads) {
+        const int v = v0 + tid;
+        long long cost = 0;
+        if (v < nv) {
+            int lo = 0, hi = batch - 1;  // the last run with first[run] <= v (runs without tokens share a first)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (first[mid] <= v)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            __align__(16) int32_t gr[kVarInts];
+            fill_group(gr, lo, v - first[lo], cu[lo], cu[lo + 1], max(seqlens[lo], 0), h_q, causal != 0);
+            int4* dst = reinterpret_cast<int4*>(groups + static_cast<size_t>(kVarInts) * v);
+            dst[0] = make_int4(gr[0], gr[1], gr[2], gr[3]);
+            dst[1] = make_int4(gr[4], gr[5], gr[6], gr[7]);
+            cost = pages_of(gr[kVarLimit]) + fixed_cost;
+        }
+        long long x = cost;
+        const int lane = tid & 31, w = tid >> 5;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_tot_ll[w] = x;
+        __syncthreads();
+        long long before = total, tile = 0;
+        for (int i = 0; i < kVarThreads / 32; ++i) {
+            if (i < w) before += warp_tot_ll[i];
+            tile += warp_tot_ll[i];
+        }
+        if (v < nv) C[v] = before + x - cost;
+        total += tile;
+        __syncthreads();
+    }
+    for (int p = tid; p < num_parts; p += kVarThreads) {
+        int32_t m[kMdInts];
+        partition_range(p, num_parts, C, nullptr, nv, total, fixed_cost, m);
+        begins[2 * p] = m[0];
+        begins[2 * p + 1] = m[1];
+        m[5] = skip ? MLA_ERR_DEVICE_CHECK : 0;
+        for (int i = 0; i < kMdInts; ++i) md[p * kMdInts + i] = m[i];
+    }
+    __syncthreads();
+    for (int p = tid; p < num_parts; p += kVarThreads) {
+        const int bv = begins[2 * p], bb = begins[2 * p + 1];
+        if (bb > 0) {
+            int idx = 1;
+            for (int q = p - 1; q >= 0 && begins[2 * q] == bv && begins[2 * q + 1] > 0; --q) ++idx;
+            md[p * kMdInts + 4] = idx;
+            atomicAdd(groups + static_cast<size_t>(kVarInts) * bv + kVarSplits, 1);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ host side
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -1787,9 +1973,8 @@ static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // zero before the first call and is left zero by every call that completes without a device
 // error; then the split LSEs and the split partial outputs.  The control block's size does
 // not depend on the problem, so calls of different sizes can share one workspace.
-static void workspace_pointers(void* workspace, int batch, int groups, int num_parts, DecodeParams& prm)
+static void workspace_pointers(void* workspace, size_t slots, DecodeParams& prm)
 {
-    const size_t slots = workspace_slots(batch, groups, num_parts);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     prm.status = reinterpret_cast<int*>(ws);
     prm.ctl = reinterpret_cast<int*>(ws + kWorkspaceHeader);
@@ -1799,10 +1984,10 @@ static void workspace_pointers(void* workspace, int batch, int groups, int num_p
     prm.o_accum = reinterpret_cast<float*>(ws + kControlBytes + 2 * small);
 }
 
-template <bool kRope, bool kFp16, bool kPadHeads, bool kFp8, bool kSparse>
+template <bool kRope, bool kFp16, bool kPadHeads, bool kFp8, bool kSparse, bool kVarlen = false>
 static cudaError_t launch_splitkv(int grid, cudaStream_t stream, const CUtensorMap* maps, const DecodeParams& prm)
 {
-    auto kern = mla_splitkv_kernel<kRope, kFp16, kPadHeads, kFp8, kSparse>;
+    auto kern = mla_splitkv_kernel<kRope, kFp16, kPadHeads, kFp8, kSparse, kVarlen>;
     const int smem = Layout<kRope, kFp8>::kSmemBytes;
     static PerDeviceOnce configured;  // the attribute is per device
     cudaError_t e = configured.run([&]() -> cudaError_t {
@@ -1954,6 +2139,82 @@ mla_status mla_get_metadata_sparse(int num_tokens, int topk, int h_q, int h_kv, 
                            num_splits, stream);
 }
 
+// Most groups that runs of total_q tokens in all can have.
+static long long varlen_groups(int batch, int total_q, int h_q)
+{
+    return static_cast<long long>(total_q) * h_q / kRowsPerGroup + batch;
+}
+
+static mla_status check_varlen(int batch, int total_q, int h_q, int h_kv, int num_parts)
+{
+    if (batch < 0 || total_q < 0 || h_q <= 0 || h_kv <= 0 || num_parts <= 0) return MLA_ERR_INVALID_ARG;
+    if (h_kv != 1 || batch > kVarMaxRuns || num_parts > kMaxVirtualBatches) return MLA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(total_q) * h_q >= (1ll << 30)) return MLA_ERR_UNSUPPORTED;  // rows are counted in int32
+    return MLA_OK;
+}
+
+size_t mla_varlen_plan_ints(int batch, int total_q, int h_q, int h_kv, int num_parts)
+{
+    if (check_varlen(batch, total_q, h_q, h_kv, num_parts) != MLA_OK) return 0;
+    // md rows, group table, cost prefixes (64 bits each)
+    return static_cast<size_t>(num_parts) * kMdInts + static_cast<size_t>(varlen_groups(batch, total_q, h_q)) * (kVarInts + 2);
+}
+
+mla_status mla_get_metadata_varlen(const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, int batch, int total_q,
+                                   int h_q, int h_kv, int causal, int num_parts, int is_fp8_kvcache, int32_t* plan,
+                                   void* stream)
+{
+    const mla_status s = check_varlen(batch, total_q, h_q, h_kv, num_parts);
+    if (s != MLA_OK) return s;
+    if (!plan || (reinterpret_cast<uintptr_t>(plan) & 15) || (causal != 0 && causal != 1) ||
+        (batch > 0 && (!cu_seqlens_q || !cache_seqlens)))
+        return MLA_ERR_INVALID_ARG;
+    const long long most = varlen_groups(batch, total_q, h_q);
+    int32_t* groups = plan + static_cast<size_t>(num_parts) * kMdInts;
+    long long* c_global = reinterpret_cast<long long*>(groups + static_cast<size_t>(most) * kVarInts);
+    constexpr size_t kMost = 200 * 1024;
+    size_t smem = (static_cast<size_t>(batch) + 2) * 4 + static_cast<size_t>(num_parts) * 8 + 16;
+    if (smem + static_cast<size_t>(most) * 8 <= kMost) {
+        smem += static_cast<size_t>(most) * 8;
+        c_global = nullptr;
+    }
+    if (smem > 48 * 1024) {
+        static PerDeviceOnce configured;
+        if (configured.run([] {
+                return cudaFuncSetAttribute(mla_metadata_varlen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kMost);
+            }) != cudaSuccess)
+            return MLA_ERR_CUDA;
+    }
+    mla_metadata_varlen_kernel<<<1, kVarThreads, smem, static_cast<cudaStream_t>(stream)>>>(
+        cu_seqlens_q, cache_seqlens, batch, total_q, h_q, causal, num_parts, is_fp8_kvcache ? kFixedCostFp8 : kFixedCost,
+        plan, groups, c_global);
+    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+mla_status mla_get_metadata_varlen_host(const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, int batch, int total_q,
+                                        int h_q, int h_kv, int causal, int num_parts, int is_fp8_kvcache, int32_t* plan)
+{
+    const mla_status s = check_varlen(batch, total_q, h_q, h_kv, num_parts);
+    if (s != MLA_OK) return s;
+    if (!plan || (causal != 0 && causal != 1) || (batch > 0 && (!cu_seqlens_q || !cache_seqlens))) return MLA_ERR_INVALID_ARG;
+    for (int b = 0; b < batch; ++b)
+        if (cu_seqlens_q[b] < 0 || cu_seqlens_q[b + 1] < cu_seqlens_q[b] || cu_seqlens_q[b + 1] > total_q || cache_seqlens[b] < 0)
+            return MLA_ERR_INVALID_ARG;
+    schedule_varlen_host(cu_seqlens_q, cache_seqlens, batch, h_q, causal != 0, num_parts,
+                         is_fp8_kvcache ? kFixedCostFp8 : kFixedCost, plan, plan + static_cast<size_t>(num_parts) * kMdInts,
+                         reinterpret_cast<long long*>(plan + static_cast<size_t>(num_parts) * kMdInts +
+                                                      static_cast<size_t>(varlen_groups(batch, total_q, h_q)) * kVarInts));
+    return MLA_OK;
+}
+
+size_t mla_decode_varlen_workspace_bytes(int num_parts)
+{
+    if (num_parts <= 0 || num_parts > kMaxVirtualBatches) return 0;
+    const size_t slots = 2 * static_cast<size_t>(num_parts);  // a partition shares its first and its last group
+    return kControlBytes + 2 * align_up(slots * kRowsPerGroup * sizeof(float), 256) + slots * kRowsPerGroup * kDv * sizeof(float);
+}
+
 size_t mla_decode_workspace_zero_bytes(int batch, int s_q, int h_q, int h_kv)
 {
     if (batch < 0 || s_q <= 0 || h_q <= 0 || h_kv <= 0 || h_q % h_kv) return 0;
@@ -1970,6 +2231,20 @@ size_t mla_decode_workspace_bytes(int batch, int s_q, int h_q, int h_kv, int num
     bytes += 2 * align_up(slots * kRowsPerGroup * sizeof(float), 256);  // split LSEs and maxima
     bytes += slots * kRowsPerGroup * kDv * sizeof(float);
     return bytes;
+}
+
+// The tensor maps of a paged cache: K: half a page (one CTA's 32 tokens), V: a page, boxes of 64
+// columns; FP8 rows are 656 bytes, K: boxes of 128 bytes, V: of 16, no swizzle.
+static bool encode_paged_kv(CUtensorMap* maps, const void* kvcache, CUtensorMapDataType dt, int d_qk, uint64_t kv_rows, bool fp8)
+{
+    const uint64_t row_bytes = static_cast<uint64_t>(d_qk) * 2;
+    return (fp8 ? encode_2d(&maps[1], kvcache, CU_TENSOR_MAP_DATA_TYPE_UINT8, kFp8Row, kv_rows, kFp8Row, 128,
+                            kPage / 2, CU_TENSOR_MAP_SWIZZLE_NONE)
+                : encode_2d(&maps[1], kvcache, dt, d_qk, kv_rows, row_bytes, 64, kPage / 2,
+                            CU_TENSOR_MAP_SWIZZLE_128B)) &&
+           (fp8 ? encode_2d(&maps[2], kvcache, CU_TENSOR_MAP_DATA_TYPE_UINT8, kFp8Row, kv_rows, kFp8Row, 16,
+                            kPage / 2, CU_TENSOR_MAP_SWIZZLE_NONE)
+                : encode_2d(&maps[2], kvcache, dt, d_qk, kv_rows, row_bytes, 64, kPage, CU_TENSOR_MAP_SWIZZLE_128B));
 }
 
 // Validates the arguments and fills the kernel parameters and tensor maps.
@@ -2034,18 +2309,14 @@ static mla_status prepare_decode(const void* q, int batch, int s_q, int h_q, int
     prm.d_qk = d_qk;
     prm.num_parts = num_parts;
     if (batch == 0) return MLA_OK;
-    workspace_pointers(workspace, batch, groups, num_parts, prm);
+    workspace_pointers(workspace, workspace_slots(batch, groups, num_parts), prm);
     if (!maps) return MLA_OK;
 
     const CUtensorMapDataType dt =
         dtype == MLA_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t row_bytes = static_cast<uint64_t>(d_qk) * 2;
     const uint64_t kv_rows = static_cast<uint64_t>(cache_rows);
-    // Q: [batch][rows][d_qk], box 64 columns x (up to) 64 rows;
-    // K: cache rows, box 64 columns x 32 tokens (half a page, one CTA's share);
-    // V: cache rows, box 64 columns x 64 tokens (a page).
-    // FP8 cache: rows of 656 bytes; K: boxes of 128 bytes x 32 rows (latent slices), V: boxes
-    // of 16 bytes x 32 rows (the scales), no swizzle.
+    // Q: [batch][rows][d_qk], box 64 columns x (up to) 64 rows
     const bool fp8 = dtype == MLA_BF16_FP8KV;
     if (sparse && !fp8) {
         // 16-bit sparse: K and V gathered row by row (tile::gather4, one-row boxes of 64 columns);
@@ -2060,13 +2331,7 @@ static mla_status prepare_decode(const void* q, int batch, int s_q, int h_q, int
     const bool ok =
         encode_3d(&maps[0], q, dt, d_qk, rows, batch, row_bytes, row_bytes * rows, 64, prm.box_rows,
                   CU_TENSOR_MAP_SWIZZLE_128B) &&
-        (fp8 ? encode_2d(&maps[1], kvcache, CU_TENSOR_MAP_DATA_TYPE_UINT8, kFp8Row, kv_rows, kFp8Row, 128,
-                         kPage / 2, CU_TENSOR_MAP_SWIZZLE_NONE)
-             : encode_2d(&maps[1], kvcache, dt, d_qk, kv_rows, row_bytes, 64, kPage / 2,
-                         CU_TENSOR_MAP_SWIZZLE_128B)) &&
-        (fp8 ? encode_2d(&maps[2], kvcache, CU_TENSOR_MAP_DATA_TYPE_UINT8, kFp8Row, kv_rows, kFp8Row, 16,
-                         kPage / 2, CU_TENSOR_MAP_SWIZZLE_NONE)
-             : encode_2d(&maps[2], kvcache, dt, d_qk, kv_rows, row_bytes, 64, kPage, CU_TENSOR_MAP_SWIZZLE_128B));
+        encode_paged_kv(maps, kvcache, dt, d_qk, kv_rows, fp8);
     return ok ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -2172,7 +2437,7 @@ mla_status mla_decode_combine(int batch, int s_q, int h_q, int h_kv, int dv, int
     prm.num_parts = num_parts;
     prm.h_q = h_q;
     prm.active_heads = effective_active_heads(active_heads, h_q);
-    workspace_pointers(workspace, batch, groups, num_parts, prm);
+    workspace_pointers(workspace, workspace_slots(batch, groups, num_parts), prm);
     return launch_combine_stage(prm, static_cast<cudaStream_t>(stream));
 }
 
@@ -2258,6 +2523,82 @@ mla_status mla_sparse_prefill(const void* q, int s_q, int h_q, int d_qk, const v
     s = launch_splitkv_stage(prm, maps, st);
     if (s != MLA_OK) return s;
     return launch_combine_stage(prm, st);
+}
+
+mla_status mla_decode_varlen(const void* q, int total_q, int h_q, int d_qk, const void* kvcache, int num_blocks,
+                             int page_size, int h_kv, const int32_t* block_table, int batch, int max_blocks_per_seq, int dv,
+                             int dtype, const int32_t* plan, int num_parts, float softmax_scale, void* o, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream)
+{
+    const mla_status s = check_varlen(batch, total_q, h_q, h_kv, num_parts);
+    if (s != MLA_OK) return s;
+    if (num_blocks <= 0 || max_blocks_per_seq <= 0) return MLA_ERR_INVALID_ARG;
+    if (dtype != MLA_BF16 && dtype != MLA_FP16 && dtype != MLA_BF16_FP8KV) return MLA_ERR_INVALID_ARG;
+    const bool fp8 = dtype == MLA_BF16_FP8KV;
+    if (page_size != kPage || (d_qk != 576 && d_qk != 512) || dv != kDv || (fp8 && d_qk != 576)) return MLA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_blocks) * kPage >= (1ll << 31)) return MLA_ERR_UNSUPPORTED;
+    if (batch == 0 || total_q == 0) return MLA_OK;
+    if (!q || !kvcache || !block_table || !plan || !o || !lse || !workspace) return MLA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(kvcache) & 15) ||
+        (reinterpret_cast<uintptr_t>(o) & 15) || (reinterpret_cast<uintptr_t>(plan) & 15) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return MLA_ERR_INVALID_ARG;
+    if (workspace_bytes < mla_decode_varlen_workspace_bytes(num_parts)) return MLA_ERR_WORKSPACE;
+    if (!(softmax_scale > 0.f)) softmax_scale = 1.0f / std::sqrt(static_cast<float>(d_qk));
+    const int rows = total_q * h_q;
+    DecodeParams prm{};
+    prm.block_table = block_table;
+    prm.md = plan;
+    prm.vgroups = plan + static_cast<size_t>(num_parts) * kMdInts;
+    prm.q = q;
+    prm.kvcache = kvcache;
+    prm.o = o;
+    prm.lse = lse;
+    prm.batch = batch;
+    prm.s_q = 1;
+    prm.h_q = h_q;
+    prm.active_heads = h_q;
+    prm.rows = rows;
+    prm.max_blocks = max_blocks_per_seq;
+    prm.num_blocks = num_blocks;
+    prm.box_rows = rows < 64 ? rows : 64;
+    prm.scale_log2 = softmax_scale * 1.4426950408889634f;
+    prm.o_align32 = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+    prm.dtype = dtype;
+    prm.d_qk = d_qk;
+    prm.num_parts = num_parts;
+    workspace_pointers(workspace, 2 * static_cast<size_t>(num_parts), prm);
+    const CUtensorMapDataType dt = dtype == MLA_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t row_bytes = static_cast<uint64_t>(d_qk) * 2;
+    CUtensorMap maps[kNumMaps];
+    if (!encode_3d(&maps[0], q, dt, d_qk, rows, 1, row_bytes, row_bytes * rows, 64, prm.box_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_paged_kv(maps, kvcache, dt, d_qk, static_cast<uint64_t>(num_blocks) * kPage, fp8))
+        return MLA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int grid = 2 * num_parts;
+    cudaError_t e;
+    if (fp8)
+        e = launch_splitkv<true, false, false, true, false, true>(grid, st, maps, prm);
+    else if (d_qk == 576)
+        e = dtype == MLA_FP16 ? launch_splitkv<true, true, false, false, false, true>(grid, st, maps, prm)
+                              : launch_splitkv<true, false, false, false, false, true>(grid, st, maps, prm);
+    else
+        e = dtype == MLA_FP16 ? launch_splitkv<false, true, false, false, false, true>(grid, st, maps, prm)
+                              : launch_splitkv<false, false, false, false, false, true>(grid, st, maps, prm);
+    if (e != cudaSuccess) return MLA_ERR_CUDA;
+    // Few groups: each has many splits, so a row's splits are read in parallel (as for the dense decode).
+    const bool split_parallel = 4 * varlen_groups(batch, total_q, h_q) < num_parts;
+    const int rows_max = rows < kRowsPerGroup ? rows : kRowsPerGroup;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    programmatic_launch(cfg, attr, dim3(num_parts, split_parallel ? rows_max : (rows_max + 3) / 4), dim3(128), 0, st);
+    if (dtype == MLA_FP16)
+        e = split_parallel ? cudaLaunchKernelEx(&cfg, mla_combine_kernel<true, true, true>, prm)
+                           : cudaLaunchKernelEx(&cfg, mla_combine_kernel<true, false, true>, prm);
+    else
+        e = split_parallel ? cudaLaunchKernelEx(&cfg, mla_combine_kernel<false, true, true>, prm)
+                           : cudaLaunchKernelEx(&cfg, mla_combine_kernel<false, false, true>, prm);
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 mla_status mla_read_device_status(void* workspace, int clear, int* device_status, void* stream)

@@ -61,6 +61,48 @@ constexpr int kFixedCostFp8 = 6;     // the same for the paged decode over an FP
 constexpr int kFixedCostSparse = 4;  // the same for the sparse decode and prefill, tuned on B200
 constexpr int kMdInts = 8;
 
+// Ragged runs of query tokens (chunks of prompts beside decode steps): run b is the query tokens
+// [cu[b], cu[b + 1]), its rows (tokens x heads) are cut into groups of 128, and a group is a virtual
+// batch, numbered run by run.  One row of the group table per virtual batch:
+enum VarField : int {
+    kVarReq = 0,     // the run (request)
+    kVarRow0 = 1,    // its first query row in the call's total_q * h_q rows
+    kVarRows = 2,    // its rows (at most 128)
+    kVarLimit = 3,   // cached rows that its last token sees: its pages end there
+    kVarSeen = 4,    // a row of token t (of the call's tokens) sees clamp(kVarSeen + t, 0, kVarLen) cached rows
+    kVarLen = 5,     // the request's cached rows
+    kVarSplits = 6,  // partitions that share it
+    kVarInts = 8
+};
+
+// Visible rows of token `tok` (of the call's tokens) of a run of tokens [t0, t1) over len cached
+// rows: the causal mask is aligned to the bottom right.
+MLA_HD inline int run_seen(int t1, int len, bool causal)
+{
+    return causal ? len - t1 + 1 : 0x40000000;
+}
+
+MLA_HD inline int clamp_seen(long long seen, int len)
+{
+    return seen < 0 ? 0 : (seen < len ? static_cast<int>(seen) : len);
+}
+
+// Group g of run b = tokens [t0, t1): its row of the table (kVarSplits = 1).
+MLA_HD inline void fill_group(int32_t* gr, int b, int g, int t0, int t1, int len, int h_q, bool causal)
+{
+    const int row0 = t0 * h_q + g * kRowsPerGroup, end = t1 * h_q;
+    const int rows = end - row0 < kRowsPerGroup ? end - row0 : kRowsPerGroup;
+    const int seen = run_seen(t1, len, causal);
+    gr[kVarReq] = b;
+    gr[kVarRow0] = row0;
+    gr[kVarRows] = rows;
+    gr[kVarLimit] = clamp_seen(static_cast<long long>(seen) + (row0 + rows - 1) / h_q, len);
+    gr[kVarSeen] = seen;
+    gr[kVarLen] = len;
+    gr[kVarSplits] = 1;
+    gr[7] = 0;
+}
+
 MLA_HD inline int row_groups(int heads_per_kv) { return (heads_per_kv + kRowsPerGroup - 1) / kRowsPerGroup; }
 
 MLA_HD inline int pages_of(int seqlen) { return seqlen <= 0 ? 0 : (seqlen + kPage - 1) / kPage; }
@@ -152,6 +194,30 @@ inline void schedule_host(const int32_t* seqlens, int batch, int groups, int num
         acc += 1 + extra;
     }
     num_splits[nv] = acc;
+}
+
+// The same for ragged runs: group table and md rows.  Scratch: C [groups].
+inline void schedule_varlen_host(const int32_t* cu, const int32_t* seqlens, int batch, int h_q, bool causal, int num_parts,
+                                 int F, int32_t* md, int32_t* groups, long long* C)
+{
+    int nv = 0;
+    long long total = 0;
+    for (int b = 0; b < batch; ++b)
+        for (int g = 0; g < row_groups((cu[b + 1] - cu[b]) * h_q); ++g, ++nv) {
+            int32_t* gr = groups + static_cast<long long>(kVarInts) * nv;
+            fill_group(gr, b, g, cu[b], cu[b + 1], seqlens[b], h_q, causal);
+            C[nv] = total;
+            total += pages_of(gr[kVarLimit]) + F;
+        }
+    for (int p = 0; p < num_parts; ++p) partition_range(p, num_parts, C, nullptr, nv, total, F, md + p * kMdInts);
+    for (int p = 0; p < num_parts; ++p) {
+        int32_t* m = md + p * kMdInts;
+        if (m[1] > 0) {
+            m[4] = 1;
+            for (int q = p - 1; q >= 0 && md[q * kMdInts] == m[0] && md[q * kMdInts + 1] > 0; --q) ++m[4];
+            ++groups[static_cast<long long>(kVarInts) * m[0] + kVarSplits];
+        }
+    }
 }
 
 }  // namespace mla
