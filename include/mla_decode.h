@@ -439,6 +439,43 @@ MLA_API mla_status mla_summarize_pages(const void* kvcache, int num_blocks, int 
                                        int32_t* device_status, void* stream);
 
 /*
+ * Page selection for block-sparse decoding: the pages whose keys (mla_summarize_pages) score best for
+ * each query token, as a block table of its own that mla_decode_with_kvcache reads with one request
+ * per token.
+ *
+ * Token t = b * s_q + s sees n = clamp(L_b - s_q + 1 + s, 0, L_b) cached rows (causal; L_b otherwise) in
+ * N = ceil(n / 64) pages.  For page j of them, P = block_table[b][j]:
+ *   s_h    = max(max_i |q[b,s,h,i]| * (1/127), 2^-126),  q8_h = q / s_h, rounded to float32, then to
+ *            the nearest whole number
+ *   score  = max over heads h of (s_h * <q8_h, page_keys[P]>), times page_scales[P]
+ *            (the inner product is a whole number, each product rounded once to float32: every
+ *            implementation gets the same bits; NaN counts as the least)
+ * The first n_first and the last n_last pages are always in (the last one may be partly filled and need
+ * have no key); the others fill topn places by score, the lower page first where scores are equal.
+ *   page_table[t]   the chosen pages' physical ids in ascending order of j, then -1   (all N when N <= topn)
+ *   page_seqlens[t] cached rows in them: 64 for each but the last, which holds n - 64 (N - 1)   (0 when n = 0)
+ *
+ *   q              device [batch, s_q, h_q, d_qk] bf16 or fp16 (dtype), 16-byte aligned; d_qk 576 or
+ *                  512, h_q <= 128
+ *   page_keys      device int8 [num_blocks, d_qk], 16-byte aligned;  page_scales device float32 [num_blocks]
+ *   block_table    device int32 [batch, max_blocks_per_seq];  cache_seqlens device int32 [batch]
+ *   topn >= n_first + n_last, n_first >= 0, n_last >= 1
+ *   page_table     device int32 [batch * s_q, topn], written;  page_seqlens device int32 [batch * s_q], written
+ *   workspace      device, >= mla_select_workspace_bytes(...), 16-byte aligned, any contents
+ *   device_status  device int32 or null: records MLA_ERR_DEVICE_CHECK for a block-table entry outside
+ *                  the cache (scored as page 0) or a length beyond the table (cut to it), MLA_ERR_TIMEOUT
+ * Enqueues two kernels on `stream`.  Then mla_get_metadata(page_seqlens, batch * s_q, h_q, 1, ...) and
+ * mla_decode_with_kvcache(q, batch * s_q, 1, h_q, ..., page_table, topn, page_seqlens, ..., causal 0).
+ */
+MLA_API size_t mla_select_workspace_bytes(int batch, int s_q, int max_blocks_per_seq);
+MLA_API mla_status mla_select_pages(const void* q, int batch, int s_q, int h_q, int d_qk, int dtype,
+                                    const int8_t* page_keys, const float* page_scales, int num_blocks,
+                                    const int32_t* block_table, int max_blocks_per_seq, const int32_t* cache_seqlens,
+                                    int causal, int topn, int n_first, int n_last, int32_t* page_table,
+                                    int32_t* page_seqlens, void* workspace, size_t workspace_bytes,
+                                    int32_t* device_status, void* stream);
+
+/*
  * Reads the device status word of a workspace (synchronises `stream`).
  * *device_status receives MLA_OK or the first device-side error recorded by a
  * decode call that used this workspace; clear != 0 then zeroes the workspace's

@@ -13,7 +13,9 @@ Public calls (the names of the pages' API; "FlashMLA" usage page, deepep.org):
 Around the decode:
 
 * :func:`mla_append_kvcache` -- new tokens' rows into the cache (norm, rotation, quantization);
-* :func:`mla_summarize_pages` -- 8-bit page keys of completed pages.
+* :func:`mla_summarize_pages` -- 8-bit page keys of completed pages;
+* :func:`mla_select_pages` -- each query token's best pages by those keys, as a block table, and
+  :func:`flash_mla_page_sparse` -- the decode over them.
 
 All are thin wrappers over the C ABI in ``include/mla_decode.h``; the kernels
 live in ``csrc/``.  ``workloads`` generates seeded synthetic inputs.
@@ -22,12 +24,13 @@ from .api import (DecodeCall, flash_mla_sparse_fwd, flash_mla_with_kvcache, get_
                   get_mla_metadata_sparse_host, metadata_sizes, num_sm_parts, read_device_status, workspace_bytes,
                   workspace_zero_bytes)
 from .cache import mla_append_kvcache, mla_summarize_pages
+from .select import flash_mla_page_sparse, mla_select_pages
 from .varlen import (VarlenPlan, flash_mla_varlen_with_kvcache, get_mla_metadata_varlen, get_mla_metadata_varlen_host,
                      varlen_workspace_bytes)
 from ._lib import MLAError
 
-__all__ = ["DecodeCall", "VarlenPlan", "flash_mla_sparse_fwd", "flash_mla_varlen_with_kvcache", "flash_mla_with_kvcache",
-           "get_mla_metadata", "get_mla_metadata_host", "get_mla_metadata_sparse_host", "get_mla_metadata_varlen",
-           "get_mla_metadata_varlen_host", "varlen_workspace_bytes",
-           "metadata_sizes", "mla_append_kvcache", "mla_summarize_pages",
-           "num_sm_parts", "read_device_status", "workspace_bytes", "workspace_zero_bytes", "MLAError"]
+__all__ = ["DecodeCall", "VarlenPlan", "flash_mla_page_sparse", "flash_mla_sparse_fwd", "flash_mla_varlen_with_kvcache",
+           "flash_mla_with_kvcache", "get_mla_metadata", "get_mla_metadata_host", "get_mla_metadata_sparse_host",
+           "get_mla_metadata_varlen", "get_mla_metadata_varlen_host", "metadata_sizes", "mla_append_kvcache",
+           "mla_select_pages", "mla_summarize_pages", "num_sm_parts", "read_device_status", "varlen_workspace_bytes",
+           "workspace_bytes", "workspace_zero_bytes", "MLAError"]

@@ -70,6 +70,11 @@ SIGNATURES = {
                            _P, _I, _I, _I, _I,          # block_table, batch, max_blocks, dv, dtype
                            _P, _I, _F,                  # plan, num_parts, scale
                            _P, _P, _P, _SZ, _P], _I),   # o, lse, workspace, ws_bytes, stream
+    "mla_select_workspace_bytes": ([_I, _I, _I], _SZ),
+    "mla_select_pages": ([_P, _I, _I, _I, _I, _I,       # q, batch, s_q, h_q, d_qk, dtype
+                          _P, _P, _I, _P, _I, _P,       # page_keys, page_scales, num_blocks, block_table, max_blocks, seqlens
+                          _I, _I, _I, _I,               # causal, topn, n_first, n_last
+                          _P, _P, _P, _SZ, _P, _P], _I),  # page_table, page_seqlens, workspace, ws_bytes, status, stream
     "mla_append_kvcache": ([_P, _LL, _P, _LL, _P, _F,        # latent, stride, k_pe, stride, norm_weight, norm_eps
                             _P, _P, _I, _P, _I,              # positions, cos_sin, max_position, slots, num_tokens
                             _P, _I, _I, _I, _I, _I, _I,      # kvcache, num_blocks, page_size, h_kv, d_qk, dtype, interleaved

@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "_mla_decode.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("mla_decode.cu", "cache_ops.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("mla_decode.cu", "cache_ops.cu", "select_pages.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("host_util.cuh", "ptx.cuh", "scheduler.cuh")] + [
     os.path.join(ROOT, "include", "mla_decode.h")]
 

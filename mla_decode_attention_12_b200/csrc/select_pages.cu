@@ -1,0 +1,596 @@
+// Page selection for block-sparse decoding: every query token scores the 8-bit keys of the pages
+// that it sees and keeps the best, as a block table of its own that the paged decode reads.
+// Formulas, layouts and errors: include/mla_decode.h.
+
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "../../include/mla_decode.h"
+#include "host_util.cuh"
+#include "ptx.cuh"
+#include "scheduler.cuh"
+
+namespace mla {
+
+constexpr int kScoreThreads = 512;
+constexpr int kTile = 128;                          // pages per tile: the rows (M) of one MMA
+constexpr int kMaxHeads = 128;                      // query heads: its columns (N), in groups of 32
+constexpr int kKeyBoxBytes = kTile * 64;            // 128 rows x 64 bytes, swizzled in 64-byte rows
+constexpr float kTinyQ = 1.17549435e-38f;           // 2^-126
+constexpr unsigned long long kScoreTimeoutNs = 2000000000ull;
+
+struct SelectParams {
+    const uint8_t* q;           // [tokens, h_q, d] 16-bit
+    const int8_t* keys;         // [num_blocks, d]
+    const float* scales;        // [num_blocks]
+    const int32_t* block_table;
+    const int32_t* seqlens;
+    float* scores;              // [tokens, max_blocks]
+    int32_t* out_table;         // [tokens, topn]
+    int32_t* out_lens;          // [tokens]
+    int* status;
+    int tokens, s_q, h_q, max_blocks, num_blocks, topn, first, last, causal;
+};
+
+// Cached rows that token t sees, at most what the block table holds.
+__device__ __forceinline__ int seen_by(const SelectParams& p, int t, bool* too_long = nullptr)
+{
+    const int b = t / p.s_q, s = t - b * p.s_q;
+    const long long len = p.seqlens[b];
+    const long long n = p.causal ? len - p.s_q + 1 + s : len;
+    const long long most = static_cast<long long>(p.max_blocks) * kPage;
+    if (too_long) *too_long = n > most;
+    return static_cast<int>(n < 0 ? 0 : (n > most ? most : n));
+}
+
+__device__ __forceinline__ int tiles_of(int n) { return (pages_of(n) + kTile - 1) / kTile; }
+
+// Asynchronous 16-byte copy into shared memory; zeros when `live` is false (nothing is read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// D(tmem) (+)= A(smem desc) * B(smem desc)^T in 8-bit whole numbers, 32-bit accumulators.
+__device__ __forceinline__ void mma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// kind::i8: signed 8-bit A and B, 32-bit accumulators, both operands K-major.
+__host__ __device__ constexpr uint32_t instr_desc_i8(int M, int N)
+{
+    return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int kD>
+struct ScoreLayout {
+    static constexpr int kBoxes = kD / 64;
+    static constexpr int kTileBytes = kBoxes * kKeyBoxBytes;  // 73.7 KB at 576
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kTileBytes;                   // two stages
+    static constexpr int kOffRed = kOffK + 2 * kTileBytes;     // [4][128] floats: column groups' maxima
+    static constexpr int kOffPid = kOffRed + 4 * kTile * 4;    // [2][128] pages
+    static constexpr int kOffQs = kOffPid + 2 * kTile * 4;     // [128] head scales
+    static constexpr int kOffBar = kOffQs + kMaxHeads * 4;
+    static constexpr int kBytes = kOffBar + 64 + 1024;
+};
+static_assert(ScoreLayout<576>::kBytes <= 232448, "shared memory plan exceeds 227 KB");
+static_assert(ScoreLayout<576>::kTileBytes % 1024 == 0 && ScoreLayout<512>::kTileBytes % 1024 == 0, "operand alignment");
+
+// Scores.  For a token's pages j, score = max over heads h of (s_h * <q8_h, key_j>) times the page's
+// scale, q8_h = rint(q_h / s_h) in [-127, 127] with s_h = max|q_h| / 127: the products are whole
+// numbers below 2^24, exact in the 8-bit tensor-core products, so the score is the same bits in any
+// order of summation, and which pages win does not depend on the kernel.
+//
+// Bound by reading the keys (580 bytes per page and request: one 127th of the page itself).  The
+// (token, tile of 128 pages) pairs of the call are laid on a line and each of the SMs takes an equal
+// run of it, so that lengths balance.  A tile's keys (rows gathered through the block table) come by
+// 16-byte asynchronous copies into the swizzled K-major layout of the MMA, two tiles in flight; the
+// MMA has the pages as rows (M = 128) and the heads as columns, so a thread of the epilogue owns a
+// page and takes the maximum over heads in its registers: no exchange between lanes.  The queries
+// are quantized once per token and CTA.
+template <int kD, bool kFp16>
+__global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const SelectParams p)
+{
+    using L = ScoreLayout<kD>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s_base = smem_addr(smem);
+    float(*red)[kTile] = reinterpret_cast<float(*)[kTile]>(smem + L::kOffRed);
+    int(*pid)[kTile] = reinterpret_cast<int(*)[kTile]>(smem + L::kOffPid);
+    float* qscale = reinterpret_cast<float*>(smem + L::kOffQs);
+    const uint32_t bar = s_base + L::kOffBar;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 16);
+    __shared__ int sh_token, sh_tile, warp_tot[kScoreThreads / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_launch_dependents();
+
+    // ---- this CTA's run [t_lo, t_hi) of the line of tiles: total first, then the token t_lo falls into
+    auto block_scan = [&](int x, int& total) {  // exclusive
+        int incl = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        __syncthreads();
+        if (lane == 31) warp_tot[warp] = incl;
+        __syncthreads();
+        int before = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kScoreThreads / 32; ++w) {
+            if (w < warp) before += warp_tot[w];
+            total += warp_tot[w];
+        }
+        return before + incl - x;
+    };
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+        sh_token = p.tokens;
+        sh_tile = 0;
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_addr(tmem_slot), 256);
+        tmem_relinquish();
+    }
+    int mine = 0;
+    for (int t = tid; t < p.tokens; t += kScoreThreads) {
+        bool too_long;
+        mine += tiles_of(seen_by(p, t, &too_long));
+        if (too_long && blockIdx.x == 0 && p.status) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
+    }
+    int line;
+    block_scan(mine, line);
+    const int t_lo = static_cast<int>(static_cast<long long>(line) * blockIdx.x / gridDim.x);
+    const int t_hi = static_cast<int>(static_cast<long long>(line) * (blockIdx.x + 1) / gridDim.x);
+    for (int t0 = 0, base = 0; t0 < p.tokens && base <= t_lo; t0 += kScoreThreads) {
+        const int x = t0 + tid < p.tokens ? tiles_of(seen_by(p, t0 + tid)) : 0;
+        int total;
+        const int at = base + block_scan(x, total);
+        if (at <= t_lo && t_lo < at + x) {
+            sh_token = t0 + tid;
+            sh_tile = t_lo - at;
+        }
+        base += total;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const int n_here = t_hi - t_lo;
+
+    // Position on the line: token, tile in it, pages that the token sees.
+    struct Place {
+        int token, tile, n;
+    };
+    auto start_of = [&](int token, int tile) { return Place{token, tile, token < p.tokens ? seen_by(p, token) : 0}; };
+    auto next_of = [&](Place a) {
+        if (a.tile + 1 < tiles_of(a.n)) return Place{a.token, a.tile + 1, a.n};
+        Place b{a.token + 1, 0, 0};
+        while (b.token < p.tokens && (b.n = seen_by(p, b.token)) == 0) ++b.token;
+        return b;
+    };
+    // the page of row tid < 128 of a tile, or -1 past the token's pages
+    auto page_at = [&](const Place& a) {
+        const int j = a.tile * kTile + tid;
+        if (a.token >= p.tokens || j >= pages_of(a.n)) return -1;
+        int page = __ldg(p.block_table + static_cast<size_t>(a.token / p.s_q) * p.max_blocks + j);
+        if (page < 0 || page >= p.num_blocks) {
+            if (p.status) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
+            page = 0;
+        }
+        return page;
+    };
+    auto load_tile = [&](int stage) {  // 16-byte words of the rows whose pages are in pid[stage]
+        const uint32_t dst = s_base + L::kOffK + stage * L::kTileBytes;
+        constexpr int kWords = kD / 16;
+#pragma unroll
+        for (int k = 0; k < kTile * kWords / kScoreThreads; ++k) {
+            const int i = tid + k * kScoreThreads;
+            const int r = i / kWords, c = i - r * kWords;
+            const int page = pid[stage][r];
+            // 64-byte swizzled rows: word c % 4 of box c / 4 goes to word (c % 4) ^ ((r / 2) % 4)
+            cp_async16(dst + (c >> 2) * kKeyBoxBytes + r * 64 + (((c & 3) ^ ((r >> 1) & 3)) << 4),
+                       p.keys + static_cast<size_t>(max(page, 0)) * kD + 16 * c, page >= 0);
+        }
+        cp_async_commit();
+    };
+    static_assert((kTile * (kD / 16)) % kScoreThreads == 0, "whole rounds of copies");
+
+    bool ok = true;
+    if (n_here > 0) {
+        Place cur = start_of(sh_token, sh_tile), nxt = next_of(cur);
+        float scale_cur = 0.f, scale_nxt = 0.f;
+        int pid_nxt = -1;
+        if (tid < kTile) {
+            const int page = page_at(cur);
+            pid[0][tid] = page;
+            scale_cur = page >= 0 ? __ldg(p.scales + page) : 0.f;
+            pid_nxt = n_here > 1 ? page_at(nxt) : -1;
+        }
+        __syncthreads();
+        load_tile(0);
+        int q_token = -1;
+        const int ncols = (p.h_q + 31) & ~31;
+        const uint32_t idesc = instr_desc_i8(kTile, ncols);
+        for (int i = 0; i < n_here; ++i) {
+            const int stage = i & 1;
+            // the next tile's copies, before this one's are awaited
+            if (i + 1 < n_here) {
+                Place after = next_of(nxt);
+                if (tid < kTile) {
+                    pid[stage ^ 1][tid] = pid_nxt;
+                    scale_nxt = pid_nxt >= 0 ? __ldg(p.scales + pid_nxt) : 0.f;
+                    pid_nxt = i + 2 < n_here ? page_at(after) : -1;
+                }
+                __syncthreads();
+                load_tile(stage ^ 1);
+                // (`nxt` moves on below)
+            }
+            if (q_token != cur.token) {
+                // The token's heads in 8 bits: a warp takes whole heads, lane l the column pairs
+                // (64 k + 2 l, + 1).  Rows past the last head are zero.
+                q_token = cur.token;
+                constexpr int kPer = kD / 64;
+                for (int h0 = warp; h0 < ncols; h0 += 4 * (kScoreThreads / 32)) {
+                    uint32_t raw[4][kPer];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int h = h0 + u * (kScoreThreads / 32);
+                        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                            p.q + (static_cast<size_t>(cur.token) * p.h_q + (h < p.h_q ? h : 0)) * kD * 2);
+#pragma unroll
+                        for (int k = 0; k < kPer; ++k) raw[u][k] = h < p.h_q ? src[32 * k + lane] : 0u;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int h = h0 + u * (kScoreThreads / 32);
+                        if (h >= ncols) break;
+                        float m = 0.f;
+                        float2 f[kPer];
+#pragma unroll
+                        for (int k = 0; k < kPer; ++k) {
+                            if constexpr (kFp16)
+                                f[k] = __half22float2(*reinterpret_cast<const __half2*>(&raw[u][k]));
+                            else
+                                f[k] = make_float2(__uint_as_float(raw[u][k] << 16), __uint_as_float(raw[u][k] & 0xffff0000u));
+                            m = fmaxf(m, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+                        }
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        const float s = fmaxf(m * (1.0f / 127.0f), kTinyQ);
+                        if (lane == 0) qscale[h] = s;
+#pragma unroll
+                        for (int k = 0; k < kPer; ++k) {
+                            const int a = max(-127, min(127, __float2int_rn(__fdiv_rn(f[k].x, s))));
+                            const int b = max(-127, min(127, __float2int_rn(__fdiv_rn(f[k].y, s))));
+                            // columns 64 k + 2 lane: word lane / 8 of box k
+                            const int w = (lane >> 3) ^ ((h >> 1) & 3);
+                            *reinterpret_cast<uint16_t*>(smem + L::kOffQ + k * kKeyBoxBytes + h * 64 + (w << 4) + 2 * (lane & 7)) =
+                                static_cast<uint16_t>((a & 0xff) | ((b & 0xff) << 8));
+                        }
+                    }
+                }
+            }
+            if (i + 1 < n_here)
+                cp_async_wait<1>();
+            else
+                cp_async_wait<0>();
+            fence_proxy_async_smem();  // this thread's copies and stores, before the tensor core reads them
+            tc_fence_before();         // (and the epilogue's loads of the tile before last are done)
+            __syncthreads();
+            if (warp == 0 && elect_one()) {
+                tc_fence_after();
+                const uint64_t a0 = smem_desc(s_base + L::kOffK + stage * L::kTileBytes, 16, 512, kLayoutSW64);
+                const uint64_t b0 = smem_desc(s_base + L::kOffQ, 16, 512, kLayoutSW64);
+#pragma unroll
+                for (int ks = 0; ks < 2 * L::kBoxes; ++ks) {  // 32 columns per step
+                    const uint32_t off = ((ks >> 1) * kKeyBoxBytes + (ks & 1) * 32) >> 4;
+                    mma_i8_ss(tmem + 128 * stage, a0 + off, b0 + off, idesc, ks > 0 ? 1u : 0u);
+                }
+                mma_commit(bar);
+            }
+            bool done = mbar_test_wait(bar, i & 1);
+            if (!done) {
+                const uint64_t start = global_timer_ns();
+                while (!(done = mbar_try_wait(bar, i & 1)) && global_timer_ns() - start < kScoreTimeoutNs) {
+                }
+            }
+            ok = __syncthreads_and(done) != 0;
+            if (!ok) break;
+            tc_fence_after();
+            // Thread (lane quarter, column group): its page's maximum over 32 heads.
+            const int row = 32 * (warp & 3) + lane, cg = warp >> 2;
+            if (32 * cg < ncols) {
+                uint32_t v[32];
+                tmem_ld32(tmem + 128 * stage + 32 * cg + (static_cast<uint32_t>(32 * (warp & 3)) << 16), v);
+                tmem_wait_ld();
+                reg_fence(v);
+                float m = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float x = __fmul_rn(static_cast<float>(static_cast<int>(v[c])), qscale[32 * cg + c]);
+                    if (32 * cg + c < p.h_q) m = fmaxf(m, x);
+                }
+                red[cg][row] = m;
+            }
+            __syncthreads();
+            if (tid < kTile) {
+                const int j = cur.tile * kTile + tid, n_pages = pages_of(cur.n);
+                float m = red[0][tid];
+                for (int c = 1; 32 * c < ncols; ++c) m = fmaxf(m, red[c][tid]);
+                float s = __fmul_rn(m, scale_cur);
+                // finite, so that nothing beats a page that is always in
+                s = s == s ? fminf(fmaxf(s, -FLT_MAX), FLT_MAX) : -FLT_MAX;
+                if (j < p.first || j >= n_pages - p.last) s = INFINITY;
+                if (j < n_pages) p.scores[static_cast<size_t>(cur.token) * p.max_blocks + j] = s;
+                scale_cur = scale_nxt;
+            }
+            if (i + 1 < n_here) {
+                cur = nxt;
+                nxt = next_of(nxt);
+            }
+        }
+    }
+    if (!ok) {
+        // A product that never completed: say so, give the copies and it time to end, and leave.
+        if (tid == 0 && p.status) atomicCAS(p.status, 0, MLA_ERR_TIMEOUT);
+        cp_async_wait<0>();
+        const uint64_t start = global_timer_ns();
+        while (global_timer_ns() - start < 50000000ull) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
+}
+
+// Selection: one CTA per token.  The topn-th largest score is found bit by bit, two bits of the
+// (order-preserving) 32-bit pattern per round: each round counts the scores at or above three
+// candidate thresholds, in registers and one exchange between warps; 16 rounds whatever the values,
+// where a histogram would serialise on scores that share their leading bits.  Thread i holds scores
+// [i * kPer, (i + 1) * kPer), so ranks by prefix sums give the pages in order and ties to the lower.
+// kPer 0: more pages than a CTA's registers hold, read again each round.
+constexpr int kSelectThreadsSmall = 256, kSelectPerSmall = 8;    // up to 2,048 pages
+constexpr int kSelectThreadsLarge = 1024, kSelectPerLarge = 16;  // up to 16,384
+
+template <int kThreads, int kPer>
+__global__ void __launch_bounds__(kThreads) mla_select_pages_kernel(const SelectParams p)
+{
+    constexpr int kWarps = kThreads / 32;
+    __shared__ int part[2][3][kWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int t = blockIdx.x;
+    grid_dependency_wait();
+    const int sees = seen_by(p, t);
+    const int n = pages_of(sees);
+    const int per = kPer > 0 ? kPer : (n + kThreads - 1) / kThreads;
+    const float* scores = p.scores + static_cast<size_t>(t) * p.max_blocks;
+    const int32_t* table = p.block_table + static_cast<size_t>(t / p.s_q) * p.max_blocks;
+    int32_t* out = p.out_table + static_cast<size_t>(t) * p.topn;
+    const int keep = min(n, p.topn);
+    for (int i = keep + tid; i < p.topn; i += kThreads) out[i] = -1;
+    if (tid == 0) p.out_lens[t] = n > 0 ? (keep - 1) * kPage + (sees - (n - 1) * kPage) : 0;
+    if (n <= p.topn) {
+        for (int i = tid; i < n; i += kThreads) out[i] = table[i];
+        return;
+    }
+    // Order-preserving pattern: larger score, larger number; 0 past the pages (below every score).
+    auto pattern = [&](int j) -> uint32_t {
+        if (j >= n) return 0u;
+        const uint32_t u = __float_as_uint(__ldcg(scores + j) + 0.0f);  // -0 counts as 0
+        return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    };
+    uint32_t key[kPer > 0 ? kPer : 1];
+    if constexpr (kPer > 0) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) key[k] = pattern(tid * kPer + k);
+    }
+    auto get = [&](int k) -> uint32_t {
+        if constexpr (kPer > 0)
+            return key[k];
+        else
+            return pattern(tid * per + k);
+    };
+    int buf = 0;
+    auto sum3 = [&](int a, int b, int c, int& ta, int& tb, int& tc) {
+        a = __reduce_add_sync(0xffffffffu, a);
+        b = __reduce_add_sync(0xffffffffu, b);
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0) {
+            part[buf][0][warp] = a;
+            part[buf][1][warp] = b;
+            part[buf][2][warp] = c;
+        }
+        __syncthreads();
+        const bool in = lane < kWarps;
+        ta = __reduce_add_sync(0xffffffffu, in ? part[buf][0][lane] : 0);
+        tb = __reduce_add_sync(0xffffffffu, in ? part[buf][1][lane] : 0);
+        tc = __reduce_add_sync(0xffffffffu, in ? part[buf][2][lane] : 0);
+        buf ^= 1;
+    };
+    uint32_t thr = 0;  // the largest pattern with at least topn scores at or above it
+    for (int bit = 30; bit >= 0; bit -= 2) {
+        const uint32_t c1 = thr | (1u << bit), c2 = thr | (2u << bit), c3 = thr | (3u << bit);
+        int a = 0, b = 0, c = 0;
+        if constexpr (kPer > 0) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                a += key[k] >= c1;
+                b += key[k] >= c2;
+                c += key[k] >= c3;
+            }
+        } else {
+            for (int k = 0; k < per; ++k) {
+                const uint32_t x = get(k);  // (0 past the pages: below every candidate)
+                a += x >= c1;
+                b += x >= c2;
+                c += x >= c3;
+            }
+        }
+        int ta, tb, tc;
+        sum3(a, b, c, ta, tb, tc);
+        thr = tc >= p.topn ? c3 : (tb >= p.topn ? c2 : (ta >= p.topn ? c1 : thr));
+    }
+    int above = 0, equal = 0;
+#pragma unroll (kPer > 0 ? kPer : 1)
+    for (int k = 0; k < per; ++k) {
+        const uint32_t x = get(k);
+        above += x > thr;
+        equal += x == thr;
+    }
+    // exclusive prefix sums of both over the threads (in page order)
+    auto scan = [&](int x, int& before, int& total) {
+        int incl = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) part[buf][0][warp] = incl;
+        __syncthreads();
+        int b = 0;
+        total = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            const int v = part[buf][0][w];
+            if (w < warp) b += v;
+            total += v;
+        }
+        before = b + incl - x;
+        buf ^= 1;
+    };
+    int above_before, above_total, equal_before, equal_total;
+    scan(above, above_before, above_total);
+    scan(equal, equal_before, equal_total);
+    const int room = p.topn - above_total;  // how many of the equal ones are in: the first
+    int at = above_before + min(equal_before, room);
+#pragma unroll (kPer > 0 ? kPer : 1)
+    for (int k = 0; k < per; ++k) {
+        const uint32_t x = get(k);
+        const bool in = x > thr || (x == thr && equal_before < room);
+        equal_before += x == thr;
+        if (in) out[at++] = table[tid * per + k];
+    }
+}
+
+template <int kD, bool kFp16>
+static cudaError_t launch_scores(int grid, cudaStream_t st, const SelectParams& prm)
+{
+    auto kern = mla_score_pages_kernel<kD, kFp16>;
+    constexpr int smem = ScoreLayout<kD>::kBytes;
+    static PerDeviceOnce configured;
+    cudaError_t e = configured.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kScoreThreads, smem, st>>>(prm);
+    return cudaGetLastError();
+}
+
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" {
+
+size_t mla_select_workspace_bytes(int batch, int s_q, int max_blocks_per_seq)
+{
+    if (batch < 0 || s_q <= 0 || max_blocks_per_seq <= 0) return 0;
+    const long long n = static_cast<long long>(batch) * s_q * max_blocks_per_seq;
+    return n >= (1ll << 40) ? 0 : static_cast<size_t>(n) * sizeof(float) + 256;
+}
+
+mla_status mla_select_pages(const void* q, int batch, int s_q, int h_q, int d_qk, int dtype, const int8_t* page_keys,
+                            const float* page_scales, int num_blocks, const int32_t* block_table, int max_blocks_per_seq,
+                            const int32_t* cache_seqlens, int causal, int topn, int n_first, int n_last,
+                            int32_t* page_table, int32_t* page_seqlens, void* workspace, size_t workspace_bytes,
+                            int32_t* device_status, void* stream)
+{
+    if (batch < 0 || s_q <= 0 || h_q <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || (causal != 0 && causal != 1))
+        return MLA_ERR_INVALID_ARG;
+    if (dtype != MLA_BF16 && dtype != MLA_FP16) return dtype == MLA_BF16_FP8KV ? MLA_ERR_UNSUPPORTED : MLA_ERR_INVALID_ARG;
+    if (n_first < 0 || n_last < 1 || topn < 1 || n_first > topn || n_last > topn - n_first) return MLA_ERR_INVALID_ARG;
+    if ((d_qk != 576 && d_qk != 512) || h_q > kMaxHeads) return MLA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_blocks) * kPage >= (1ll << 31) || static_cast<long long>(max_blocks_per_seq) * kPage >= (1ll << 31))
+        return MLA_ERR_UNSUPPORTED;
+    const long long tokens = static_cast<long long>(batch) * s_q;
+    // the line of tiles is counted in int32
+    if (tokens * ((max_blocks_per_seq + kTile - 1) / kTile) >= (1ll << 31) || tokens >= (1ll << 31) / h_q) return MLA_ERR_UNSUPPORTED;
+    if (batch == 0) return MLA_OK;
+    if (!q || !page_keys || !page_scales || !block_table || !cache_seqlens || !page_table || !page_seqlens || !workspace)
+        return MLA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(page_keys) & 15) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 15))
+        return MLA_ERR_INVALID_ARG;
+    if (workspace_bytes < mla_select_workspace_bytes(batch, s_q, max_blocks_per_seq)) return MLA_ERR_WORKSPACE;
+    int sms = 0;
+    if (!sm_count(&sms)) return MLA_ERR_CUDA;
+    SelectParams prm{};
+    prm.q = static_cast<const uint8_t*>(q);
+    prm.keys = page_keys;
+    prm.scales = page_scales;
+    prm.block_table = block_table;
+    prm.seqlens = cache_seqlens;
+    prm.scores = static_cast<float*>(workspace);
+    prm.out_table = page_table;
+    prm.out_lens = page_seqlens;
+    prm.status = device_status;
+    prm.tokens = static_cast<int>(tokens);
+    prm.s_q = s_q;
+    prm.h_q = h_q;
+    prm.max_blocks = max_blocks_per_seq;
+    prm.num_blocks = num_blocks;
+    prm.topn = topn;
+    prm.first = n_first;
+    prm.last = n_last;
+    prm.causal = causal;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const long long most = tokens * ((max_blocks_per_seq + kTile - 1) / kTile);
+    const int grid = most < sms ? static_cast<int>(most) : sms;
+    cudaError_t e;
+    if (d_qk == 576)
+        e = dtype == MLA_FP16 ? launch_scores<576, true>(grid, st, prm) : launch_scores<576, false>(grid, st, prm);
+    else
+        e = dtype == MLA_FP16 ? launch_scores<512, true>(grid, st, prm) : launch_scores<512, false>(grid, st, prm);
+    if (e != cudaSuccess) return MLA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(tokens));
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (max_blocks_per_seq <= kSelectThreadsSmall * kSelectPerSmall) {
+        cfg.blockDim = dim3(kSelectThreadsSmall);
+        e = cudaLaunchKernelEx(&cfg, mla_select_pages_kernel<kSelectThreadsSmall, kSelectPerSmall>, prm);
+    } else if (max_blocks_per_seq <= kSelectThreadsLarge * kSelectPerLarge) {
+        cfg.blockDim = dim3(kSelectThreadsLarge);
+        e = cudaLaunchKernelEx(&cfg, mla_select_pages_kernel<kSelectThreadsLarge, kSelectPerLarge>, prm);
+    } else {
+        cfg.blockDim = dim3(kSelectThreadsLarge);
+        e = cudaLaunchKernelEx(&cfg, mla_select_pages_kernel<kSelectThreadsLarge, 0>, prm);
+    }
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // extern "C"

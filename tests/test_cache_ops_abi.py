@@ -57,3 +57,30 @@ def test_summarize_refuses(lib, over, code):
 
 def test_summarize_of_no_requests_is_a_no_op(lib):
     assert summarize(lib, batch=0, kvcache=None) == 0
+
+
+def select(lib, **over):
+    a = dict(q=FAKE, batch=2, s_q=1, h_q=16, d_qk=576, dtype=0, keys=FAKE, scales=FAKE, num_blocks=8, table=FAKE, max_blocks=4,
+             lens=FAKE, causal=1, topn=3, first=1, last=1, out=FAKE, out_lens=FAKE, ws=FAKE, ws_bytes=1 << 40, status=None,
+             stream=None)
+    a.update(over)
+    return lib.mla_select_pages(*a.values())
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(q=None), 1), (dict(keys=None), 1), (dict(scales=None), 1), (dict(table=None), 1), (dict(lens=None), 1),
+    (dict(out=None), 1), (dict(out_lens=None), 1), (dict(ws=None), 1), (dict(batch=-1), 1), (dict(s_q=0), 1), (dict(h_q=0), 1),
+    (dict(max_blocks=0), 1), (dict(num_blocks=0), 1), (dict(causal=2), 1), (dict(dtype=7), 1), (dict(topn=0), 1),
+    (dict(topn=1), 1), (dict(last=0), 1), (dict(first=-1), 1), (dict(first=2 ** 31 - 1, topn=2 ** 31 - 1), 1),
+    (dict(q=FAKE + 2), 1), (dict(keys=FAKE + 4), 1), (dict(ws=FAKE + 8), 1),
+    (dict(dtype=2), 2), (dict(d_qk=192), 2), (dict(h_q=129), 2), (dict(num_blocks=1 << 26), 2), (dict(max_blocks=1 << 26), 2),
+    (dict(batch=1 << 28), 2), (dict(ws_bytes=16), 3),
+])
+def test_select_refuses(lib, over, code):
+    assert select(lib, **over) == code
+
+
+def test_select_of_no_requests_is_a_no_op(lib):
+    assert select(lib, batch=0, q=None) == 0
+    assert lib.mla_select_workspace_bytes(2, 3, 10) >= 2 * 3 * 10 * 4
+    assert lib.mla_select_workspace_bytes(2, 0, 10) == 0
