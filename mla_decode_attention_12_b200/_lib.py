@@ -87,6 +87,7 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_binding = None
 
 
 class MLAError(RuntimeError):
@@ -119,6 +120,22 @@ def bind(path: str) -> ctypes.CDLL:
         fn.argtypes = argtypes
         fn.restype = restype
     return lib
+
+
+def binding():
+    """The compiled PyTorch binding ``_mla_torch.so``; raises if it is missing (built with the library)."""
+    global _binding
+    if _binding is None:
+        load()
+        try:
+            import torch  # noqa: F401  (its libraries come first)
+
+            from . import _mla_torch
+        except ImportError as e:
+            raise ImportError("the PyTorch binding _mla_torch.so is missing or does not load: build it with "
+                              f"`python -m mla_decode_attention_12_b200.build` ({e})") from e
+        _binding = _mla_torch
+    return _binding
 
 
 def status_string(status: int) -> str:

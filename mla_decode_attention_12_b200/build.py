@@ -1,4 +1,5 @@
-"""Builds the C-ABI shared library ``_mla_decode.so`` in-tree with nvcc for sm_100a.
+"""Builds the C-ABI shared library ``_mla_decode.so`` in-tree with nvcc for sm_100a, and the
+PyTorch binding ``_mla_torch.so`` beside it.
 
 Usage: ``python -m mla_decode_attention_12_b200.build`` (or call :func:`build`).
 The CUDA runtime is linked statically, so the library needs only the NVIDIA
@@ -9,14 +10,19 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "_mla_decode.so")
+BINDING = os.path.join(HERE, "_mla_torch.so")
+BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
+HEADER = os.path.join(ROOT, "include", "mla_decode.h")
 SOURCES = [os.path.join(CSRC, f) for f in ("mla_decode.cu", "cache_ops.cu", "select_pages.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("host_util.cuh", "ptx.cuh", "scheduler.cuh")] + [
-    os.path.join(ROOT, "include", "mla_decode.h")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("host_util.cuh", "ptx.cuh", "scheduler.cuh")] + [HEADER]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -31,11 +37,11 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def up_to_date(out: str = LIB) -> bool:
+def up_to_date(out: str = LIB, deps=None) -> bool:
     if not os.path.exists(out):
         return False
     t = os.path.getmtime(out)
-    return all(os.path.getmtime(d) <= t for d in DEPS)
+    return all(os.path.getmtime(d) <= t for d in (DEPS if deps is None else deps))
 
 
 def build(force: bool = False, verbose: bool = False, extra=(), out: str = LIB) -> str:
@@ -43,16 +49,56 @@ def build(force: bool = False, verbose: bool = False, extra=(), out: str = LIB) 
 
     ``extra`` adds nvcc flags and ``out`` names another file: instrumented or test-only
     builds of the same sources (``-DMLA_TIMELINE``, ``-DMLA_TEST_WITHHOLD_K_PAGE=n``) go
-    to their own files, never to the product library's."""
-    if not force and up_to_date(out):
-        return out
+    to their own files, never to the product library's.  The product build includes the
+    PyTorch binding."""
+    todo = []
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-o", tmp, *SOURCES]
+    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor() as pool:
+        if force or not up_to_date(out):
+            objs = [os.path.join(objects, os.path.basename(src) + ".o") for src in SOURCES]
+            flags = [f for f in NVCC_FLAGS if f != "-shared"]
+            todo = [pool.submit(_run, [nvcc(), *flags, *extra, "-I", os.path.join(ROOT, "include"), "-c", "-o", obj, src], verbose)
+                    for src, obj in zip(SOURCES, objs)]
+        binding = None
+        if out == LIB and (force or not up_to_date(BINDING, [BINDING_SOURCE, HEADER])):
+            binding = os.path.join(objects, "binding.o")
+            todo.append(pool.submit(_compile_binding, binding, verbose))
+        for t in todo:
+            t.result()
+        if len(todo) > (binding is not None):
+            _run([nvcc(), *NVCC_FLAGS, "-o", tmp, *objs], verbose)
+            os.replace(tmp, out)
+        if binding is not None:
+            _link_binding(binding, verbose)
+    return out
+
+
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
-    os.replace(tmp, out)
-    return out
+
+
+def _torch_dir() -> str:
+    import torch
+
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_binding(obj: str, verbose: bool) -> None:
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=1",
+          *(f for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), cuda, sysconfig.get_paths()["include"])
+            for f in ("-isystem", d)), "-c", "-o", obj, BINDING_SOURCE], verbose)
+
+
+def _link_binding(obj: str, verbose: bool) -> None:
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:_mla_decode.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10", "-lc10_cuda",
+          "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"], verbose)
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

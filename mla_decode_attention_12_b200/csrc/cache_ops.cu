@@ -271,9 +271,26 @@ struct SummarizeParams {
     int batch, max_blocks, num_blocks, d;
 };
 
-constexpr int kSumPhases = 4;                            // threads that share a column group: 16 rows each
-constexpr int kSumThreads = 72 * kSumPhases;             // 72 groups of 8 columns
-constexpr int kSumChunk = 256;                           // requests per prefix sum
+// One half page (32 rows) per stage of a ring that one thread keeps full by bulk copies.
+constexpr int kSumPhases = 4;                            // threads that share a column group: 8 rows of a stage each
+constexpr int kSumWorkers = 72 * kSumPhases;             // 72 groups of 8 columns
+constexpr int kSumThreads = kSumWorkers + 32;            // and the loader's warp
+constexpr int kSumChunk = 1024;                          // requests per prefix sum
+constexpr unsigned long long kSumTimeoutNs = 2000000000ull;
+
+template <bool kFp8>
+struct SumLayout {
+    static constexpr int kStageBytes = 32 * (kFp8 ? kFp8RowBytes : 1152);  // (narrower rows use less of it)
+    static constexpr int kStages = kFp8 ? 8 : 5;
+    static constexpr int kOffPart = kStages * kStageBytes;                 // [phases][576] doubles
+    static constexpr int kOffFirst = kOffPart + kSumPhases * 576 * 8;      // [kSumChunk] first page, [kSumChunk + 1] prefix
+    static constexpr int kOffBar = kOffFirst + (2 * kSumChunk + 2) * 4;
+    static constexpr int kOffPage = kOffBar + 2 * kStages * 8;             // page of each stage
+    static constexpr int kBytes = kOffPage + kStages * 4 + 128;
+};
+static_assert(SumLayout<false>::kBytes <= 232448 && SumLayout<true>::kBytes <= 232448, "shared memory plan exceeds 227 KB");
+static_assert(SumLayout<false>::kStageBytes % 128 == 0 && SumLayout<true>::kStageBytes % 128 == 0 &&
+                  SumLayout<false>::kOffBar % 8 == 0 && SumLayout<true>::kOffBar % 8 == 0, "alignment");
 
 // Exact sum of two floats: s = fl(a + b), and what was rounded away.
 __device__ __forceinline__ float two_sum(float a, float b, float& err)
@@ -284,161 +301,235 @@ __device__ __forceinline__ float two_sum(float a, float b, float& err)
     return s;
 }
 
+// Bounded wait for a phase of an mbarrier.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity)
+{
+    if (mbar_test_wait(bar, parity)) return true;
+    const uint64_t start = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - start > kSumTimeoutNs) return false;
+    return true;
+}
+
 // Key of a page: the mean of its 64 rows, as 8-bit whole numbers and a scale.  Bound by reading
 // the page (73.7 KB of 16-bit rows).  The key's rounding must not depend on the order of the sum,
 // so the sum is kept to about 48 bits: rows are added in pairs (two_sum, 32 bits), the pairs'
 // sums in 64 bits and what they rounded away in 32; a conversion to 64 bits per value instead of
 // per pair would take as long as the reads (16 conversions per clock and SM).
-// A block takes whole pages, every gridDim-th of the list of completed pages that all blocks
-// derive alike (prefix sums over requests).  Thread (g, phase) adds columns [8 g, 8 g + 8) of
-// rows [16 phase, 16 phase + 16), 8 rows in flight; the phases meet in shared memory.
+// One block per SM takes every gridDim-th of the list of completed pages, which all blocks derive
+// alike (prefix sums over requests).  The loader's thread looks the pages up and keeps the ring of
+// half pages full by bulk copies (a page's rows are contiguous), so that 180 KB are in flight
+// while earlier rows are added; thread (g, phase) adds columns [8 g, 8 g + 8) of 8 rows of a stage,
+// and the phases meet in shared memory once per page.
 template <bool kFp16, bool kFp8>
-__global__ void __launch_bounds__(kSumThreads) mla_summarize_kernel(const SummarizeParams p)
+__global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const SummarizeParams p)
 {
-    __shared__ int first[kSumChunk], offset[kSumChunk + 1];
+    using L = SumLayout<kFp8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    double(*part)[576] = reinterpret_cast<double(*)[576]>(smem + L::kOffPart);
+    int* first = reinterpret_cast<int*>(smem + L::kOffFirst);
+    int* offset = first + kSumChunk;
+    volatile int* page_of = reinterpret_cast<volatile int*>(smem + L::kOffPage);
+    const uint32_t s_base = smem_addr(smem);
+    const uint32_t full = s_base + L::kOffBar, empty = full + 8 * L::kStages;
     __shared__ int warp_sum[kSumThreads / 32];
-    __shared__ double part[kSumPhases][kLatent + kRopeCols];
-    __shared__ float warp_max[kSumThreads / 32];
-    const int tid = threadIdx.x;
+    __shared__ float warp_max[kSumWorkers / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = tid % 72, phase = tid / 72;
-    const int groups = p.d / 8;
+    const int stride = kFp8 ? kFp8RowBytes : p.d * 2;
+    if (tid == 0) {
+        for (int i = 0; i < L::kStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, kSumWorkers / 32);
+        }
+        fence_mbar_init();
+    }
+    uint32_t stage = 0, parity = 0;  // of the loader, or of a worker
+    auto advance = [&] {
+        if (++stage == L::kStages) {
+            stage = 0;
+            parity ^= 1u;
+        }
+    };
     long long base = 0;  // pages of earlier chunks of requests
+    bool ok = true;
     for (int b0 = 0; b0 < p.batch; b0 += kSumChunk) {
         // pages [before / 64, after / 64) of each request are complete now and were not before
-        int n = 0;
-        if (tid < kSumChunk && b0 + tid < p.batch) {
-            const int lo = max(p.before[b0 + tid], 0) / kPage, hi = max(p.after[b0 + tid], 0) / kPage;
-            if (hi > p.max_blocks && p.status && blockIdx.x == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
-            n = max(min(hi, p.max_blocks) - lo, 0);
-            first[tid] = lo;
-        }
-        int x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if ((tid & 31) >= o) x += y;
-        }
-        if ((tid & 31) == 31) warp_sum[tid >> 5] = x;
-        __syncthreads();
-        int before_me = 0;
-        for (int w = 0; w < (tid >> 5); ++w) before_me += warp_sum[w];
-        if (tid < kSumChunk) offset[tid + 1] = before_me + x;
-        if (tid == 0) offset[0] = 0;
-        __syncthreads();
-        const int total = offset[kSumChunk];
-        // this block's pages among [base, base + total)
-        const long long skip = (static_cast<long long>(blockIdx.x) - base % gridDim.x + gridDim.x) % gridDim.x;
-        for (long long i = skip; i < total; i += gridDim.x) {
-            int lo = 0, hi = kSumChunk - 1;  // the last request with offset <= i
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (offset[mid] <= i)
-                    lo = mid;
-                else
-                    hi = mid - 1;
+        const int here = min(kSumChunk, p.batch - b0);
+        int total = 0;
+        for (int r0 = 0; r0 < here; r0 += kSumThreads) {
+            int n = 0;
+            const int r = r0 + tid;
+            if (r < here) {
+                const int lo = max(p.before[b0 + r], 0) / kPage, hi = max(p.after[b0 + r], 0) / kPage;
+                if (hi > p.max_blocks && p.status && blockIdx.x == 0) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
+                n = max(min(hi, p.max_blocks) - lo, 0);
+                first[r] = lo;
             }
-            const int j = first[lo] + static_cast<int>(i) - offset[lo];
-            const int page = p.block_table[static_cast<size_t>(b0 + lo) * p.max_blocks + j];
-            if (page < 0 || page >= p.num_blocks) {  // the same for the whole block
-                if (tid == 0 && p.status) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
-                continue;
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
             }
-            double acc[8];
-            float rest[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) acc[k] = 0.0, rest[k] = 0.f;
-            auto add_pair = [&](const float (&a)[8], const float (&b)[8]) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float e;
-                    acc[k] += static_cast<double>(two_sum(a[k], b[k], e));
-                    rest[k] += e;
-                }
-            };
-            if (g < groups) {
-                if (kFp8 && g < kLatent / 8) {
-                    const uint8_t* row = p.cache + (static_cast<size_t>(page) * kPage + 16 * phase) * kFp8RowBytes;
-#pragma unroll
-                    for (int r0 = 0; r0 < 16; r0 += 8) {
-                        uint2 raw[8];
-                        float sc[8];
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) {
-                            raw[r] = __ldg(reinterpret_cast<const uint2*>(row + (r0 + r) * kFp8RowBytes) + g);
-                            sc[r] = __ldg(reinterpret_cast<const float*>(row + (r0 + r) * kFp8RowBytes + kFp8ScaleOff) + g / 16);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 8; r += 2) {
-                            float v[2][8];
-#pragma unroll
-                            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const uint32_t w = k < 2 ? raw[r + q].x : raw[r + q].y;
-                                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                                        static_cast<__nv_fp8x2_storage_t>(w >> (16 * (k & 1))), __NV_E4M3);
-                                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                                    const float2 b = unpack16<false>(pack16<false>(f.x * sc[r + q], f.y * sc[r + q]));
-                                    v[q][2 * k] = b.x;
-                                    v[q][2 * k + 1] = b.y;
-                                }
-                            add_pair(v[0], v[1]);
-                        }
-                    }
-                } else {
-                    // 16-bit columns: a 16-bit row's, or an FP8 row's position columns
-                    const int stride = kFp8 ? kFp8RowBytes : p.d * 2;
-                    const uint8_t* row = p.cache + (static_cast<size_t>(page) * kPage + 16 * phase) * stride +
-                                         (kFp8 ? kFp8RopeOff + 16 * (g - kLatent / 8) : 16 * g);
-#pragma unroll
-                    for (int r0 = 0; r0 < 16; r0 += 8) {
-                        uint4 raw[8];
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) raw[r] = __ldg(reinterpret_cast<const uint4*>(row + (r0 + r) * stride));
-#pragma unroll
-                        for (int r = 0; r < 8; r += 2) {
-                            float v0[8], v1[8];
-                            unpack8<kFp16>(raw[r], v0);
-                            unpack8<kFp16>(raw[r + 1], v1);
-                            add_pair(v0, v1);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) part[phase][8 * g + k] = acc[k] + static_cast<double>(rest[k]);
-            }
+            if (lane == 31) warp_sum[warp] = x;
             __syncthreads();
-            // columns 2 tid, 2 tid + 1: the mean, rounded once to 32 bits
-            float m0 = 0.f, m1 = 0.f;
-            if (2 * tid < p.d) {
-                double s0 = 0.0, s1 = 0.0;
-#pragma unroll
-                for (int q = 0; q < kSumPhases; ++q) {
-                    s0 += part[q][2 * tid];
-                    s1 += part[q][2 * tid + 1];
-                }
-                m0 = static_cast<float>(s0 * (1.0 / kPage));
-                m1 = static_cast<float>(s1 * (1.0 / kPage));
+            int before_me = total;
+            for (int w = 0; w < kSumThreads / 32; ++w) {
+                if (w < warp) before_me += warp_sum[w];
+                total += warp_sum[w];
             }
-            float mx = fmaxf(fabsf(m0), fabsf(m1));
+            if (r < here) offset[r] = before_me + x - n;
+            __syncthreads();
+        }
+        // this block's pages among [base, base + total): i = skip, skip + gridDim, ...
+        const int skip = static_cast<int>((static_cast<long long>(blockIdx.x) - base % gridDim.x + gridDim.x) % gridDim.x);
+        if (warp == kSumWorkers / 32) {
+            if (lane == 0) {
+                for (long long i = skip; i < total && ok; i += gridDim.x) {
+                    int lo = 0, hi = here - 1;  // the last request with offset <= i
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (offset[mid] <= i)
+                            lo = mid;
+                        else
+                            hi = mid - 1;
+                    }
+                    const int j = first[lo] + static_cast<int>(i) - offset[lo];
+                    int page = p.block_table[static_cast<size_t>(b0 + lo) * p.max_blocks + j];
+                    if (page < 0 || page >= p.num_blocks) {
+                        if (p.status) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
+                        page = -1;
+                    }
+                    for (int half = 0; half < 2 && ok; ++half, advance()) {
+                        if (!(ok = wait_for(empty + 8 * stage, parity ^ 1))) break;
+                        page_of[stage] = page;
+                        if (page < 0) {
+                            mbar_arrive(full + 8 * stage);
+                        } else {
+                            mbar_arrive_expect_tx(full + 8 * stage, 32 * stride);
+                            bulk_load(s_base + stage * L::kStageBytes,
+                                      p.cache + (static_cast<size_t>(page) * kPage + 32 * half) * stride, 32 * stride,
+                                      full + 8 * stage);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        } else {
+            for (long long i = skip; i < total; i += gridDim.x) {
+                double acc[8];
+                float rest[8];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if ((tid & 31) == 0) warp_max[tid >> 5] = mx;
-            __syncthreads();  // also: part may be written again
+                for (int k = 0; k < 8; ++k) acc[k] = 0.0, rest[k] = 0.f;
+                auto add_pair = [&](const float (&a)[8], const float (&b)[8]) {
 #pragma unroll
-            for (int w = 0; w < kSumThreads / 32; ++w) mx = fmaxf(mx, warp_max[w]);
-            const float scale = fmaxf(mx * (1.0f / 127.0f), kTinyScale);
-            if (2 * tid < p.d) {
-                const int k0 = max(-127, min(127, __float2int_rn(__fdiv_rn(m0, scale))));
-                const int k1 = max(-127, min(127, __float2int_rn(__fdiv_rn(m1, scale))));
-                reinterpret_cast<char2*>(p.keys + static_cast<size_t>(page) * p.d)[tid] =
-                    make_char2(static_cast<char>(k0), static_cast<char>(k1));
-                if (tid == 0) p.scales[page] = scale;
+                    for (int k = 0; k < 8; ++k) {
+                        float e;
+                        acc[k] += static_cast<double>(two_sum(a[k], b[k], e));
+                        rest[k] += e;
+                    }
+                };
+                int page = -1;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half, advance()) {
+                    ok = ok && wait_for(full + 8 * stage, parity);
+                    page = ok ? page_of[stage] : -1;
+                    const uint8_t* row = smem + stage * L::kStageBytes + 8 * phase * stride;
+                    if (page >= 0 && 8 * g < p.d) {
+                        if (kFp8 && g < kLatent / 8) {
+#pragma unroll
+                            for (int r = 0; r < 8; r += 2) {
+                                float v[2][8];
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    const uint2 raw = *reinterpret_cast<const uint2*>(row + (r + q) * kFp8RowBytes + 8 * g);
+                                    const float sc =
+                                        *reinterpret_cast<const float*>(row + (r + q) * kFp8RowBytes + kFp8ScaleOff + 4 * (g / 16));
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const uint32_t w = k < 2 ? raw.x : raw.y;
+                                        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                                            static_cast<__nv_fp8x2_storage_t>(w >> (16 * (k & 1))), __NV_E4M3);
+                                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                                        const float2 b = unpack16<false>(pack16<false>(f.x * sc, f.y * sc));
+                                        v[q][2 * k] = b.x;
+                                        v[q][2 * k + 1] = b.y;
+                                    }
+                                }
+                                add_pair(v[0], v[1]);
+                            }
+                        } else {
+                            // 16-bit columns: a 16-bit row's, or an FP8 row's position columns
+                            const uint8_t* col = row + (kFp8 ? kFp8RopeOff + 16 * (g - kLatent / 8) : 16 * g);
+#pragma unroll
+                            for (int r = 0; r < 8; r += 2) {
+                                float v0[8], v1[8];
+                                unpack8<kFp16>(*reinterpret_cast<const uint4*>(col + r * stride), v0);
+                                unpack8<kFp16>(*reinterpret_cast<const uint4*>(col + (r + 1) * stride), v1);
+                                add_pair(v0, v1);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty + 8 * stage);
+                }
+                if (page >= 0 && 8 * g < p.d)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) part[phase][8 * g + k] = acc[k] + static_cast<double>(rest[k]);
+                named_barrier_sync(1, kSumWorkers);
+                // columns 2 tid, 2 tid + 1: the mean, rounded once to 32 bits
+                float m0 = 0.f, m1 = 0.f;
+                if (2 * tid < p.d) {
+                    double s0 = 0.0, s1 = 0.0;
+#pragma unroll
+                    for (int q = 0; q < kSumPhases; ++q) {
+                        s0 += part[q][2 * tid];
+                        s1 += part[q][2 * tid + 1];
+                    }
+                    m0 = static_cast<float>(s0 * (1.0 / kPage));
+                    m1 = static_cast<float>(s1 * (1.0 / kPage));
+                }
+                float mx = fmaxf(fabsf(m0), fabsf(m1));
+#pragma unroll
+                for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                if (lane == 0) warp_max[warp] = mx;
+                named_barrier_sync(1, kSumWorkers);  // also: part may be written again
+#pragma unroll
+                for (int w = 0; w < kSumWorkers / 32; ++w) mx = fmaxf(mx, warp_max[w]);
+                const float scale = fmaxf(mx * (1.0f / 127.0f), kTinyScale);
+                if (2 * tid < p.d && page >= 0) {
+                    const int k0 = max(-127, min(127, __float2int_rn(__fdiv_rn(m0, scale))));
+                    const int k1 = max(-127, min(127, __float2int_rn(__fdiv_rn(m1, scale))));
+                    reinterpret_cast<char2*>(p.keys + static_cast<size_t>(page) * p.d)[tid] =
+                        make_char2(static_cast<char>(k0), static_cast<char>(k1));
+                    if (tid == 0) p.scales[page] = scale;
+                }
             }
         }
         base += total;
         __syncthreads();  // first and offset may be written again
     }
+    if (!ok) {  // a copy that never came: say so, and give those in flight time to land
+        if (p.status) atomicCAS(p.status, 0, MLA_ERR_TIMEOUT);
+        const uint64_t start = global_timer_ns();
+        while (global_timer_ns() - start < 50000000ull) {
+        }
+    }
+}
+
+template <bool kFp16, bool kFp8>
+static cudaError_t launch_summarize(int grid, cudaStream_t st, const SummarizeParams& prm)
+{
+    auto kern = mla_summarize_kernel<kFp16, kFp8>;
+    constexpr int smem = SumLayout<kFp8>::kBytes;
+    static PerDeviceOnce configured;
+    const cudaError_t e =
+        configured.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kSumThreads, smem, st>>>(prm);
+    return cudaGetLastError();
 }
 
 }  // namespace mla
@@ -555,15 +646,12 @@ mla_status mla_summarize_pages(const void* kvcache, int num_blocks, int page_siz
     prm.num_blocks = num_blocks;
     prm.d = d_qk;
     const long long most = static_cast<long long>(batch) * max_blocks_per_seq;  // no more pages than that
-    const dim3 grid(static_cast<unsigned>(most < 2ll * sms ? most : 2ll * sms));
+    const int grid = most < sms ? static_cast<int>(most) : sms;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (fp8)
-        mla_summarize_kernel<false, true><<<grid, kSumThreads, 0, st>>>(prm);
-    else if (dtype == MLA_FP16)
-        mla_summarize_kernel<true, false><<<grid, kSumThreads, 0, st>>>(prm);
-    else
-        mla_summarize_kernel<false, false><<<grid, kSumThreads, 0, st>>>(prm);
-    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    const cudaError_t e = fp8 ? launch_summarize<false, true>(grid, st, prm)
+                              : (dtype == MLA_FP16 ? launch_summarize<true, false>(grid, st, prm)
+                                                   : launch_summarize<false, false>(grid, st, prm));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // extern "C"

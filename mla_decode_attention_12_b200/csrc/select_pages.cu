@@ -78,6 +78,17 @@ __host__ __device__ constexpr uint32_t instr_desc_i8(int M, int N)
     return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// x / s, rounded to float32 and then to the nearest whole number, |x| <= 127 s up to rounding.  The
+// product with the reciprocal is within 2^-22 of the quotient, relative: it rounds to the same
+// number unless it lies that close to the middle between two, where the division decides (about one
+// value in 8,000; a division for each took longer than the rest of the token's set-up).
+__device__ __forceinline__ int quantized(float x, float s, float inv)
+{
+    float y = __fmul_rn(x, inv);
+    if (fabsf(fabsf(__fsub_rn(y, rintf(y))) - 0.5f) < 6.1e-5f) y = __fdiv_rn(x, s);  // 127 * 2^-21 = 6.06e-5
+    return max(-127, min(127, __float2int_rn(y)));
+}
+
 template <int kD>
 struct ScoreLayout {
     static constexpr int kBoxes = kD / 64;
@@ -277,11 +288,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const
 #pragma unroll
                         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                         const float s = fmaxf(m * (1.0f / 127.0f), kTinyQ);
+                        const float inv = __frcp_rn(s);
                         if (lane == 0) qscale[h] = s;
 #pragma unroll
                         for (int k = 0; k < kPer; ++k) {
-                            const int a = max(-127, min(127, __float2int_rn(__fdiv_rn(f[k].x, s))));
-                            const int b = max(-127, min(127, __float2int_rn(__fdiv_rn(f[k].y, s))));
+                            const int a = quantized(f[k].x, s, inv), b = quantized(f[k].y, s, inv);
                             // columns 64 k + 2 lane: word lane / 8 of box k
                             const int w = (lane >> 3) ^ ((h >> 1) & 3);
                             *reinterpret_cast<uint16_t*>(smem + L::kOffQ + k * kKeyBoxBytes + h * 64 + (w << 4) + 2 * (lane & 7)) =

@@ -8,8 +8,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .api import _DTYPES, _ptr, _stream, flash_mla_with_kvcache, get_mla_metadata
-from .cache import _check_ints, _check_status, check_page_keys
+from .api import flash_mla_with_kvcache, get_mla_metadata
 
 
 def mla_select_pages(q: torch.Tensor, page_keys: torch.Tensor, page_scales: torch.Tensor, block_table: torch.Tensor,
@@ -26,30 +25,10 @@ def mla_select_pages(q: torch.Tensor, page_keys: torch.Tensor, page_scales: torc
     a block table for ``flash_mla_with_kvcache`` with one request per token and ``page_seqlens`` as its
     lengths.  ``status`` int32 [1]: receives a device-side error.
     """
-    dev = q.device
-    if not q.is_cuda or q.dtype not in _DTYPES or q.dim() != 4 or not q.is_contiguous():
-        raise ValueError("q must be contiguous bfloat16 or float16 [b, s_q, h_q, d_qk] on a CUDA device")
-    b, s_q, h_q, d_qk = q.shape
-    if page_keys.dim() != 2:
-        raise ValueError("page_keys must be int8 [num_blocks, d_qk]")
-    num_blocks = page_keys.shape[0]
-    check_page_keys(page_keys, page_scales, num_blocks, d_qk, dev)
-    _check_ints(dev, block_table=(block_table, 2), cache_seqlens=(cache_seqlens, 1))
-    _check_status(status, dev)
-    if block_table.shape[0] != b or cache_seqlens.shape[0] != b:
-        raise ValueError("inconsistent shapes")
-    table = torch.empty(b * s_q, max(0, topn), dtype=torch.int32, device=dev)
-    lens = torch.empty(b * s_q, dtype=torch.int32, device=dev)
-    lib = _lib.load()
-    ws_bytes = lib.mla_select_workspace_bytes(b, s_q, block_table.shape[1])
-    if ws_bytes == 0:
-        raise ValueError("invalid or unsupported sizes for the selection")
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _lib.check(lib.mla_select_pages(_ptr(q), b, s_q, h_q, d_qk, _DTYPES[q.dtype], _ptr(page_keys), _ptr(page_scales),
-                                        num_blocks, _ptr(block_table), block_table.shape[1], _ptr(cache_seqlens),
-                                        int(bool(causal)), topn, n_first, n_last, _ptr(table), _ptr(lens), _ptr(ws), ws_bytes,
-                                        _ptr(status), _stream(dev)), "mla_select_pages")
+    st, table, lens = _lib.binding().select(q, page_keys, page_scales, block_table, cache_seqlens, topn, n_first, n_last,
+                                            bool(causal), status)
+    if st:
+        _lib.check(st, "mla_select_pages")
     return table, lens
 
 

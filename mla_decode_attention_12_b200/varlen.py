@@ -5,18 +5,15 @@ Formulas and errors: ``include/mla_decode.h``.
 """
 from __future__ import annotations
 
-import math
-from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
 from . import _lib
-from .api import _DTYPES, _ptr, _stream, get_workspace, num_sm_parts, workspace_zero_bytes
-from .cache import _cache_dtype, _check_ints
+from .api import get_workspace, workspace_zero_bytes
 
 
-@dataclass(frozen=True)
-class VarlenPlan:
+class VarlenPlan(NamedTuple):
     """A step's schedule (device memory) and the sizes that it was made for."""
     data: torch.Tensor   # int32, opaque
     batch: int
@@ -35,28 +32,17 @@ def get_mla_metadata_varlen(cu_seqlens_q: torch.Tensor, cache_seqlens: torch.Ten
     of ``total_q``; ``cache_seqlens`` int32 [batch]: cached tokens of each request, the run's own included.
     ``out``: a plan of the same sizes, written again (for captured graphs).
     """
-    dev = cu_seqlens_q.device
-    if not cu_seqlens_q.is_cuda:
-        raise ValueError("cu_seqlens_q must be on a CUDA device")
-    _check_ints(dev, cu_seqlens_q=(cu_seqlens_q, 1), cache_seqlens=(cache_seqlens, 1))
-    batch = cache_seqlens.shape[0]
-    if cu_seqlens_q.shape[0] != batch + 1:
-        raise ValueError("cu_seqlens_q must have one entry more than cache_seqlens")
-    if num_parts is None:
-        num_parts = out.num_parts if out is not None else num_sm_parts(dev)
-    lib = _lib.load()
-    ints = lib.mla_varlen_plan_ints(batch, total_q, h_q, h_kv, num_parts)
-    if ints == 0:
-        raise ValueError("invalid or unsupported sizes for the schedule")
-    plan = VarlenPlan(out.data if out is not None else torch.empty(ints, dtype=torch.int32, device=dev), batch, int(total_q),
-                      int(h_q), num_parts, bool(causal))
-    if out is not None and (out != plan or out.data.device != dev or out.data.numel() != ints):
-        raise ValueError("out is a plan of other sizes")
-    with torch.cuda.device(dev):
-        _lib.check(lib.mla_get_metadata_varlen(_ptr(cu_seqlens_q), _ptr(cache_seqlens), batch, total_q, h_q, h_kv,
-                                               int(plan.causal), num_parts, int(bool(is_fp8_kvcache)), _ptr(plan.data),
-                                               _stream(dev)), "mla_get_metadata_varlen")
-    return plan
+    causal = bool(causal)
+    if out is not None:
+        if (out.batch, out.total_q, out.h_q, out.causal) != (cache_seqlens.numel(), total_q, h_q, causal) or \
+                num_parts not in (None, out.num_parts):
+            raise ValueError("out is a plan of other sizes")
+        num_parts = out.num_parts
+    st, parts, data = _lib.binding().varlen_plan(cu_seqlens_q, cache_seqlens, total_q, h_q, h_kv, causal, bool(is_fp8_kvcache),
+                                                 num_parts, None if out is None else out.data)
+    if st:
+        _lib.check(st, "mla_get_metadata_varlen")
+    return VarlenPlan(data, cache_seqlens.shape[0], total_q, h_q, parts, causal)
 
 
 def get_mla_metadata_varlen_host(cu_seqlens_q, cache_seqlens, h_q: int, h_kv: int = 1, *, causal: bool = True,
@@ -86,16 +72,25 @@ def varlen_workspace_bytes(num_parts: int) -> int:
     return n
 
 
-def _call_workspace(nbytes: int, dev: torch.device) -> torch.Tensor:
+_varlen_bytes: dict = {}  # workspace size by partition count
+
+
+def _call_workspace(num_parts: int, dev: torch.device) -> torch.Tensor:
     """The stream's cached workspace; inside a graph capture one of the graph's own, whose control block each replay
     zeroes (two graphs captured on one stream may be replayed on two)."""
-    zero = workspace_zero_bytes(1, 1, 1, 1)
-    with torch.cuda.device(dev):
-        if not torch.cuda.is_current_stream_capturing():
-            return get_workspace(nbytes, dev, zero)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        ws[:zero].zero_()
-        return ws
+    if dev.type != "cuda":
+        raise ValueError("q must be on a CUDA device")
+    sizes = _varlen_bytes.get(num_parts)
+    if sizes is None:
+        sizes = _varlen_bytes[num_parts] = (varlen_workspace_bytes(num_parts), workspace_zero_bytes(1, 1, 1, 1))
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call_workspace(num_parts, dev)
+    if not torch.cuda.is_current_stream_capturing():
+        return get_workspace(sizes[0], dev, sizes[1])
+    ws = torch.empty(sizes[0], dtype=torch.uint8, device=dev)
+    ws[:sizes[1]].zero_()
+    return ws
 
 
 def flash_mla_varlen_with_kvcache(q: torch.Tensor, kvcache: torch.Tensor, block_table: torch.Tensor,
@@ -111,37 +106,14 @@ def flash_mla_varlen_with_kvcache(q: torch.Tensor, kvcache: torch.Tensor, block_
     with the same ``cu_seqlens_q``, ``cache_seqlens`` and ``causal``.  Rows past ``cu_seqlens_q[batch]`` are
     not written (of ``out`` and ``lse`` passed in, they stay as they were).
     """
-    dtype, d_qk = _cache_dtype(kvcache, is_fp8_kvcache)
-    dev = kvcache.device
-    dt = torch.bfloat16 if is_fp8_kvcache else kvcache.dtype
-    if q.dim() != 3 or q.dtype != dt or q.shape[2] != d_qk or not q.is_contiguous() or q.device != dev:
-        raise ValueError(f"q must be contiguous {dt} [total_q, h_q, {d_qk}] on {dev}")
-    total_q, h_q, _ = q.shape
-    _check_ints(dev, block_table=(block_table, 2), cu_seqlens_q=(cu_seqlens_q, 1), cache_seqlens=(cache_seqlens, 1))
-    batch = cache_seqlens.shape[0]
-    if block_table.shape[0] != batch or cu_seqlens_q.shape[0] != batch + 1:
-        raise ValueError("inconsistent shapes")
-    if (plan.batch, plan.total_q, plan.h_q, plan.causal) != (batch, total_q, h_q, bool(causal)) or plan.data.device != dev:
-        raise ValueError("the plan was made for another call")
-    if out is None:
-        out = torch.empty(total_q, h_q, dv, dtype=dt, device=dev)
-    elif out.dtype != dt or tuple(out.shape) != (total_q, h_q, dv) or not out.is_contiguous() or out.device != dev:
-        raise ValueError(f"out must be contiguous {dt} [{total_q}, {h_q}, {dv}] on {dev}")
-    if lse is None:
-        lse = torch.empty(total_q, h_q, dtype=torch.float32, device=dev)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (total_q, h_q) or not lse.is_contiguous() or lse.device != dev:
-        raise ValueError(f"lse must be contiguous float32 [{total_q}, {h_q}] on {dev}")
+    data, batch, total_q, h_q, num_parts, planned_causal = plan
+    if q.dim() != 3 or (batch, total_q, h_q, planned_causal) != (cache_seqlens.numel(), q.shape[0], q.shape[1], bool(causal)):
+        raise ValueError("the plan was made for another call, or q is not [total_q, h_q, d_qk]")
     if workspace is None:
-        workspace = _call_workspace(varlen_workspace_bytes(plan.num_parts), dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {dev}")
-    if batch == 0 or total_q == 0:
-        return out, lse
-    num_blocks, page, h_kv, _ = kvcache.shape
-    scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(d_qk)
-    with torch.cuda.device(dev):
-        _lib.check(_lib.load().mla_decode_varlen(
-            _ptr(q), total_q, h_q, d_qk, _ptr(kvcache), num_blocks, page, h_kv, _ptr(block_table), batch,
-            block_table.shape[1], dv, dtype, _ptr(plan.data), plan.num_parts, scale, _ptr(out), _ptr(lse), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(dev)), "mla_decode_varlen")
+        workspace = _call_workspace(num_parts, q.device)
+    scale = 0.0 if softmax_scale is None else softmax_scale  # 0: 1 / sqrt(d_qk)
+    st, out, lse = _lib.binding().varlen(q, kvcache, block_table, cu_seqlens_q, cache_seqlens, dv, data, num_parts, scale,
+                                         bool(is_fp8_kvcache), workspace, out, lse)
+    if st:
+        _lib.check(st, "mla_decode_varlen")
     return out, lse
