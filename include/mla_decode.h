@@ -464,10 +464,10 @@ MLA_API mla_status mla_summarize_pages(const void* kvcache, int num_blocks, int 
  *   workspace      device, >= mla_select_workspace_bytes(...), 16-byte aligned, any contents
  *   device_status  device int32 or null: records MLA_ERR_DEVICE_CHECK for a block-table entry outside
  *                  the cache (scored as page 0) or a length beyond the table (cut to it), MLA_ERR_TIMEOUT
- * Enqueues two kernels on `stream`.  Then mla_get_metadata(page_seqlens, batch * s_q, h_q, 1, ...) and
+ * Enqueues three kernels on `stream`.  Then mla_get_metadata(page_seqlens, batch * s_q, h_q, 1, ...) and
  * mla_decode_with_kvcache(q, batch * s_q, 1, h_q, ..., page_table, topn, page_seqlens, ..., causal 0).
  */
-MLA_API size_t mla_select_workspace_bytes(int batch, int s_q, int max_blocks_per_seq);
+MLA_API size_t mla_select_workspace_bytes(int batch, int s_q, int h_q, int d_qk, int max_blocks_per_seq);
 MLA_API mla_status mla_select_pages(const void* q, int batch, int s_q, int h_q, int d_qk, int dtype,
                                     const int8_t* page_keys, const float* page_scales, int num_blocks,
                                     const int32_t* block_table, int max_blocks_per_seq, const int32_t* cache_seqlens,

@@ -70,7 +70,7 @@ SIGNATURES = {
                            _P, _I, _I, _I, _I,          # block_table, batch, max_blocks, dv, dtype
                            _P, _I, _F,                  # plan, num_parts, scale
                            _P, _P, _P, _SZ, _P], _I),   # o, lse, workspace, ws_bytes, stream
-    "mla_select_workspace_bytes": ([_I, _I, _I], _SZ),
+    "mla_select_workspace_bytes": ([_I, _I, _I, _I, _I], _SZ),
     "mla_select_pages": ([_P, _I, _I, _I, _I, _I,       # q, batch, s_q, h_q, d_qk, dtype
                           _P, _P, _I, _P, _I, _P,       # page_keys, page_scales, num_blocks, block_table, max_blocks, seqlens
                           _I, _I, _I, _I,               # causal, topn, n_first, n_last

@@ -272,7 +272,8 @@ struct SummarizeParams {
 };
 
 // One half page (32 rows) per stage of a ring that one thread keeps full by bulk copies.
-constexpr int kSumPhases = 4;                            // threads that share a column group: 8 rows of a stage each
+constexpr int kSumPhases = 8;                            // threads that share a column group: 4 rows of a stage each
+constexpr int kSumRows = 32 / kSumPhases;
 constexpr int kSumWorkers = 72 * kSumPhases;             // 72 groups of 8 columns
 constexpr int kSumThreads = kSumWorkers + 32;            // and the loader's warp
 constexpr int kSumChunk = 1024;                          // requests per prefix sum
@@ -281,9 +282,9 @@ constexpr unsigned long long kSumTimeoutNs = 2000000000ull;
 template <bool kFp8>
 struct SumLayout {
     static constexpr int kStageBytes = 32 * (kFp8 ? kFp8RowBytes : 1152);  // (narrower rows use less of it)
-    static constexpr int kStages = kFp8 ? 8 : 5;
-    static constexpr int kOffPart = kStages * kStageBytes;                 // [phases][576] doubles
-    static constexpr int kOffFirst = kOffPart + kSumPhases * 576 * 8;      // [kSumChunk] first page, [kSumChunk + 1] prefix
+    static constexpr int kStages = kFp8 ? 7 : 4;
+    static constexpr int kOffPart = kStages * kStageBytes;                 // [phases][8][73] doubles
+    static constexpr int kOffFirst = kOffPart + kSumPhases * 8 * 73 * 8;   // [kSumChunk] first page, [kSumChunk + 1] prefix
     static constexpr int kOffBar = kOffFirst + (2 * kSumChunk + 2) * 4;
     static constexpr int kOffPage = kOffBar + 2 * kStages * 8;             // page of each stage
     static constexpr int kBytes = kOffPage + kStages * 4 + 128;
@@ -318,8 +319,8 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity)
 // per pair would take as long as the reads (16 conversions per clock and SM).
 // One block per SM takes every gridDim-th of the list of completed pages, which all blocks derive
 // alike (prefix sums over requests).  The loader's thread looks the pages up and keeps the ring of
-// half pages full by bulk copies (a page's rows are contiguous), so that 180 KB are in flight
-// while earlier rows are added; thread (g, phase) adds columns [8 g, 8 g + 8) of 8 rows of a stage,
+// half pages full by bulk copies (a page's rows are contiguous), so that up to 147 KB are in flight
+// while earlier rows are added; thread (g, phase) adds columns [8 g, 8 g + 8) of 4 rows of a stage,
 // and the phases meet in shared memory once per page.
 template <bool kFp16, bool kFp8>
 __global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const SummarizeParams p)
@@ -327,7 +328,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const Sum
     using L = SumLayout<kFp8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    double(*part)[576] = reinterpret_cast<double(*)[576]>(smem + L::kOffPart);
+    // partial sum of column 8 g + k: part[phase][k][g] (rows of 73: neighbouring threads on other banks)
+    double(*part)[8][73] = reinterpret_cast<double(*)[8][73]>(smem + L::kOffPart);
     int* first = reinterpret_cast<int*>(smem + L::kOffFirst);
     int* offset = first + kSumChunk;
     volatile int* page_of = reinterpret_cast<volatile int*>(smem + L::kOffPage);
@@ -436,11 +438,11 @@ __global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const Sum
                 for (int half = 0; half < 2; ++half, advance()) {
                     ok = ok && wait_for(full + 8 * stage, parity);
                     page = ok ? page_of[stage] : -1;
-                    const uint8_t* row = smem + stage * L::kStageBytes + 8 * phase * stride;
+                    const uint8_t* row = smem + stage * L::kStageBytes + kSumRows * phase * stride;
                     if (page >= 0 && 8 * g < p.d) {
                         if (kFp8 && g < kLatent / 8) {
 #pragma unroll
-                            for (int r = 0; r < 8; r += 2) {
+                            for (int r = 0; r < kSumRows; r += 2) {
                                 float v[2][8];
 #pragma unroll
                                 for (int q = 0; q < 2; ++q) {
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const Sum
                             // 16-bit columns: a 16-bit row's, or an FP8 row's position columns
                             const uint8_t* col = row + (kFp8 ? kFp8RopeOff + 16 * (g - kLatent / 8) : 16 * g);
 #pragma unroll
-                            for (int r = 0; r < 8; r += 2) {
+                            for (int r = 0; r < kSumRows; r += 2) {
                                 float v0[8], v1[8];
                                 unpack8<kFp16>(*reinterpret_cast<const uint4*>(col + r * stride), v0);
                                 unpack8<kFp16>(*reinterpret_cast<const uint4*>(col + (r + 1) * stride), v1);
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const Sum
                 }
                 if (page >= 0 && 8 * g < p.d)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) part[phase][8 * g + k] = acc[k] + static_cast<double>(rest[k]);
+                    for (int k = 0; k < 8; ++k) part[phase][k][g] = acc[k] + static_cast<double>(rest[k]);
                 named_barrier_sync(1, kSumWorkers);
                 // columns 2 tid, 2 tid + 1: the mean, rounded once to 32 bits
                 float m0 = 0.f, m1 = 0.f;
@@ -485,8 +487,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const Sum
                     double s0 = 0.0, s1 = 0.0;
 #pragma unroll
                     for (int q = 0; q < kSumPhases; ++q) {
-                        s0 += part[q][2 * tid];
-                        s1 += part[q][2 * tid + 1];
+                        s0 += part[q][(2 * tid) & 7][tid >> 2];
+                        s1 += part[q][(2 * tid + 1) & 7][tid >> 2];
                     }
                     m0 = static_cast<float>(s0 * (1.0 / kPage));
                     m1 = static_cast<float>(s1 * (1.0 / kPage));

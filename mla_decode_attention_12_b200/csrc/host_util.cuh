@@ -42,4 +42,20 @@ struct PerDeviceOnce {
     }
 };
 
+// Launch configuration with programmatic stream serialization: the grid may start
+// while the previous one in the stream finishes; each kernel calls
+// grid_dependency_wait() before it reads global memory that grid could have written.
+inline void programmatic_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, dim3 grid, dim3 block,
+                                size_t smem, cudaStream_t stream)
+{
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+}
+
 }  // namespace mla

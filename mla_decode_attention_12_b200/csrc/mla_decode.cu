@@ -1936,22 +1936,6 @@ static bool encode_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dt
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launch configuration with programmatic stream serialization: the grid may start
-// while the previous one in the stream finishes; each kernel calls
-// grid_dependency_wait() before it reads global memory that grid could have written.
-static void programmatic_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, dim3 grid, dim3 block,
-                                size_t smem, cudaStream_t stream)
-{
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-}
-
 // Heads [active_heads, h_q) are padding whose outputs nobody reads: a count that is not a
 // multiple of 8 in (0, h_q], or an h_q that is not a multiple of 8, means every head (fail
 // closed to the full computation, as the "FlashMLA vLLM Optimization" page's active-head

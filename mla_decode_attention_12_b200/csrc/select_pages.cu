@@ -30,6 +30,8 @@ struct SelectParams {
     const int32_t* block_table;
     const int32_t* seqlens;
     float* scores;              // [tokens, max_blocks]
+    int8_t* q8;                 // [tokens, h_q, d] queries in 8 bits, and their scales
+    float* q8_scales;           // [tokens, h_q]
     int32_t* out_table;         // [tokens, topn]
     int32_t* out_lens;          // [tokens]
     int* status;
@@ -78,17 +80,73 @@ __host__ __device__ constexpr uint32_t instr_desc_i8(int M, int N)
     return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// x / s, rounded to float32 and then to the nearest whole number, |x| <= 127 s up to rounding.  The
-// product with the reciprocal is within 2^-22 of the quotient, relative: it rounds to the same
-// number unless it lies that close to the middle between two, where the division decides (about one
-// value in 8,000; a division for each took longer than the rest of the token's set-up).
-__device__ __forceinline__ int quantized(float x, float s, float inv)
+// ------------------------------------------------------------------ queries in 8 bits
+// One warp per (token, head): s = max|q| / 127, q8 = q / s rounded to float32 and then to the nearest
+// whole number.  The product with the reciprocal is within 3 * 2^-24 of the rounded quotient, relative,
+// so at most 2.3e-5 off: it rounds to the same number unless it lies that close to the middle
+// between two.  A lane that has such a value (one in 500) divides all of its values instead.
+// Rounding by adding 1.5 * 2^23: the low byte of the sum's pattern is the whole number.
+// A kernel of its own: the CTAs of the scoring kernel that share a token would otherwise each do this
+// again, which took longer than their reads.
+constexpr int kQuantThreads = 256;
+
+__device__ __noinline__ int divided(float x, float s) { return __float2int_rn(__fdiv_rn(x, s)); }
+
+template <int kD, bool kFp16>
+__global__ void __launch_bounds__(kQuantThreads) mla_quantize_queries_kernel(const SelectParams p)
 {
-    float y = __fmul_rn(x, inv);
-    if (fabsf(fabsf(__fsub_rn(y, rintf(y))) - 0.5f) < 6.1e-5f) y = __fdiv_rn(x, s);  // 127 * 2^-21 = 6.06e-5
-    return max(-127, min(127, __float2int_rn(y)));
+    constexpr int kPer = kD / 64;
+    const int lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
+    grid_launch_dependents();
+    if (row >= static_cast<long long>(p.tokens) * p.h_q) return;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + row * kD * 2);
+    float2 f[kPer];  // columns 64 k + 2 lane, + 1
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const uint32_t raw = __ldg(src + 32 * k + lane);
+        if constexpr (kFp16)
+            f[k] = __half22float2(*reinterpret_cast<const __half2*>(&raw));
+        else
+            f[k] = make_float2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xffff0000u));
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) m = fmaxf(m, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float s = fmaxf(m * (1.0f / 127.0f), kTinyQ), inv = __frcp_rn(s);
+    uint32_t w[kPer];
+    bool close = !(s < 1.0e38f);  // not finite: the division's answers
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const float y0 = __fmul_rn(f[k].x, inv), y1 = __fmul_rn(f[k].y, inv);
+        const float t0 = __fadd_rn(y0, 12582912.f), t1 = __fadd_rn(y1, 12582912.f);
+        const float d0 = __fsub_rn(y0, __fsub_rn(t0, 12582912.f)), d1 = __fsub_rn(y1, __fsub_rn(t1, 12582912.f));
+        close |= fabsf(d0) > 0.49997f || fabsf(d1) > 0.49997f;
+        w[k] = __byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x0040);
+    }
+    if (close) {
+#pragma unroll 1
+        for (int k = 0; k < kPer; ++k) {
+            // (indexed at run time only here: read again instead of keeping the registers addressable)
+            const uint32_t raw = __ldg(src + 32 * k + lane);
+            float2 x;
+            if constexpr (kFp16)
+                x = __half22float2(*reinterpret_cast<const __half2*>(&raw));
+            else
+                x = make_float2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xffff0000u));
+            const int a = max(-127, min(127, divided(x.x, s))), b = max(-127, min(127, divided(x.y, s)));
+            reinterpret_cast<uint16_t*>(p.q8 + row * kD)[32 * k + lane] = static_cast<uint16_t>((a & 0xff) | ((b & 0xff) << 8));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) reinterpret_cast<uint16_t*>(p.q8 + row * kD)[32 * k + lane] = static_cast<uint16_t>(w[k]);
+    }
+    if (lane == 0) p.q8_scales[row] = s;
 }
 
+// ------------------------------------------------------------------ scores
 template <int kD>
 struct ScoreLayout {
     static constexpr int kBoxes = kD / 64;
@@ -112,10 +170,10 @@ static_assert(ScoreLayout<576>::kTileBytes % 1024 == 0 && ScoreLayout<512>::kTil
 // Bound by reading the keys (580 bytes per page and request: one 127th of the page itself).  The
 // (token, tile of 128 pages) pairs of the call are laid on a line and each of the SMs takes an equal
 // run of it, so that lengths balance.  A tile's keys (rows gathered through the block table) come by
-// 16-byte asynchronous copies into the swizzled K-major layout of the MMA, two tiles in flight; the
+// 16-byte asynchronous copies into the swizzled K-major layout of the MMA, two tiles in flight (the
+// first while the queries are still being quantized: programmatic launch); the
 // MMA has the pages as rows (M = 128) and the heads as columns, so a thread of the epilogue owns a
-// page and takes the maximum over heads in its registers: no exchange between lanes.  The queries
-// are quantized once per token and CTA.
+// page and takes the maximum over heads in its registers: no exchange between lanes.
 template <int kD, bool kFp16>
 __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const SelectParams p)
 {
@@ -226,6 +284,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const
     };
     static_assert((kTile * (kD / 16)) % kScoreThreads == 0, "whole rounds of copies");
 
+    // (What is read before grid_dependency_wait was written before the quantizing kernel started.)
     bool ok = true;
     if (n_here > 0) {
         Place cur = start_of(sh_token, sh_tile), nxt = next_of(cur);
@@ -239,14 +298,29 @@ __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const
         }
         __syncthreads();
         load_tile(0);
+        grid_dependency_wait();
         int q_token = -1;
         const int ncols = (p.h_q + 31) & ~31;
         const uint32_t idesc = instr_desc_i8(kTile, ncols);
         for (int i = 0; i < n_here; ++i) {
             const int stage = i & 1;
+            if (q_token != cur.token) {
+                // The token's heads, in the layout of the tiles.  Rows past the last head are zero.
+                // (The earlier token's products are done: its last tile's scores are out.)
+                q_token = cur.token;
+                constexpr int kWords = kD / 16;
+                const int8_t* src = p.q8 + static_cast<size_t>(cur.token) * p.h_q * kD;
+                for (int w = tid; w < ncols * kWords; w += kScoreThreads) {
+                    const int h = w / kWords, c = w - h * kWords;
+                    cp_async16(s_base + L::kOffQ + (c >> 2) * kKeyBoxBytes + h * 64 + (((c & 3) ^ ((h >> 1) & 3)) << 4),
+                               src + (h < p.h_q ? 16 * w : 0), h < p.h_q);
+                }
+                if (tid < ncols) qscale[tid] = tid < p.h_q ? __ldcg(p.q8_scales + static_cast<size_t>(cur.token) * p.h_q + tid) : 0.f;
+                cp_async_commit();
+            }
             // the next tile's copies, before this one's are awaited
             if (i + 1 < n_here) {
-                Place after = next_of(nxt);
+                const Place after = next_of(nxt);
                 if (tid < kTile) {
                     pid[stage ^ 1][tid] = pid_nxt;
                     scale_nxt = pid_nxt >= 0 ? __ldg(p.scales + pid_nxt) : 0.f;
@@ -254,57 +328,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const
                 }
                 __syncthreads();
                 load_tile(stage ^ 1);
-                // (`nxt` moves on below)
-            }
-            if (q_token != cur.token) {
-                // The token's heads in 8 bits: a warp takes whole heads, lane l the column pairs
-                // (64 k + 2 l, + 1).  Rows past the last head are zero.
-                q_token = cur.token;
-                constexpr int kPer = kD / 64;
-                for (int h0 = warp; h0 < ncols; h0 += 4 * (kScoreThreads / 32)) {
-                    uint32_t raw[4][kPer];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int h = h0 + u * (kScoreThreads / 32);
-                        const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                            p.q + (static_cast<size_t>(cur.token) * p.h_q + (h < p.h_q ? h : 0)) * kD * 2);
-#pragma unroll
-                        for (int k = 0; k < kPer; ++k) raw[u][k] = h < p.h_q ? src[32 * k + lane] : 0u;
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int h = h0 + u * (kScoreThreads / 32);
-                        if (h >= ncols) break;
-                        float m = 0.f;
-                        float2 f[kPer];
-#pragma unroll
-                        for (int k = 0; k < kPer; ++k) {
-                            if constexpr (kFp16)
-                                f[k] = __half22float2(*reinterpret_cast<const __half2*>(&raw[u][k]));
-                            else
-                                f[k] = make_float2(__uint_as_float(raw[u][k] << 16), __uint_as_float(raw[u][k] & 0xffff0000u));
-                            m = fmaxf(m, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
-                        }
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        const float s = fmaxf(m * (1.0f / 127.0f), kTinyQ);
-                        const float inv = __frcp_rn(s);
-                        if (lane == 0) qscale[h] = s;
-#pragma unroll
-                        for (int k = 0; k < kPer; ++k) {
-                            const int a = quantized(f[k].x, s, inv), b = quantized(f[k].y, s, inv);
-                            // columns 64 k + 2 lane: word lane / 8 of box k
-                            const int w = (lane >> 3) ^ ((h >> 1) & 3);
-                            *reinterpret_cast<uint16_t*>(smem + L::kOffQ + k * kKeyBoxBytes + h * 64 + (w << 4) + 2 * (lane & 7)) =
-                                static_cast<uint16_t>((a & 0xff) | ((b & 0xff) << 8));
-                        }
-                    }
-                }
-            }
-            if (i + 1 < n_here)
                 cp_async_wait<1>();
-            else
+            } else {
                 cp_async_wait<0>();
+            }
             fence_proxy_async_smem();  // this thread's copies and stores, before the tensor core reads them
             tc_fence_before();         // (and the epilogue's loads of the tile before last are done)
             __syncthreads();
@@ -361,6 +388,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const
             }
         }
     }
+    if (n_here <= 0) grid_dependency_wait();  // no CTA, and so not the grid, ends before the quantizing one
     if (!ok) {
         // A product that never completed: say so, give the copies and it time to end, and leave.
         if (tid == 0 && p.status) atomicCAS(p.status, 0, MLA_ERR_TIMEOUT);
@@ -513,8 +541,15 @@ static cudaError_t launch_scores(int grid, cudaStream_t st, const SelectParams& 
     static PerDeviceOnce configured;
     cudaError_t e = configured.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (e != cudaSuccess) return e;
-    kern<<<grid, kScoreThreads, smem, st>>>(prm);
-    return cudaGetLastError();
+    const long long rows = static_cast<long long>(prm.tokens) * prm.h_q;
+    constexpr int kWarps = kQuantThreads / 32;
+    mla_quantize_queries_kernel<kD, kFp16><<<static_cast<unsigned>((rows + kWarps - 1) / kWarps), kQuantThreads, 0, st>>>(prm);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    programmatic_launch(cfg, attr, dim3(grid), dim3(kScoreThreads), smem, st);
+    return cudaLaunchKernelEx(&cfg, kern, prm);
 }
 
 }  // namespace mla
@@ -523,11 +558,14 @@ using namespace mla;
 
 extern "C" {
 
-size_t mla_select_workspace_bytes(int batch, int s_q, int max_blocks_per_seq)
+size_t mla_select_workspace_bytes(int batch, int s_q, int h_q, int d_qk, int max_blocks_per_seq)
 {
-    if (batch < 0 || s_q <= 0 || max_blocks_per_seq <= 0) return 0;
-    const long long n = static_cast<long long>(batch) * s_q * max_blocks_per_seq;
-    return n >= (1ll << 40) ? 0 : static_cast<size_t>(n) * sizeof(float) + 256;
+    if (batch < 0 || s_q <= 0 || h_q <= 0 || d_qk <= 0 || max_blocks_per_seq <= 0) return 0;
+    // queries in 8 bits, their scales, the scores
+    const double most = static_cast<double>(batch) * s_q * (static_cast<double>(h_q) * (d_qk + 4.0) + 4.0 * max_blocks_per_seq);
+    if (most >= 1e15) return 0;
+    const size_t tokens = static_cast<size_t>(batch) * s_q;
+    return tokens * (static_cast<size_t>(h_q) * (d_qk + 4) + 4 * static_cast<size_t>(max_blocks_per_seq)) + 256;
 }
 
 mla_status mla_select_pages(const void* q, int batch, int s_q, int h_q, int d_qk, int dtype, const int8_t* page_keys,
@@ -552,7 +590,7 @@ mla_status mla_select_pages(const void* q, int batch, int s_q, int h_q, int d_qk
     if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(page_keys) & 15) ||
         (reinterpret_cast<uintptr_t>(workspace) & 15))
         return MLA_ERR_INVALID_ARG;
-    if (workspace_bytes < mla_select_workspace_bytes(batch, s_q, max_blocks_per_seq)) return MLA_ERR_WORKSPACE;
+    if (workspace_bytes < mla_select_workspace_bytes(batch, s_q, h_q, d_qk, max_blocks_per_seq)) return MLA_ERR_WORKSPACE;
     int sms = 0;
     if (!sm_count(&sms)) return MLA_ERR_CUDA;
     SelectParams prm{};
@@ -561,7 +599,10 @@ mla_status mla_select_pages(const void* q, int batch, int s_q, int h_q, int d_qk
     prm.scales = page_scales;
     prm.block_table = block_table;
     prm.seqlens = cache_seqlens;
-    prm.scores = static_cast<float*>(workspace);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    prm.q8 = reinterpret_cast<int8_t*>(ws);
+    prm.q8_scales = reinterpret_cast<float*>(ws + static_cast<size_t>(tokens) * h_q * d_qk);  // d_qk: a multiple of 16
+    prm.scores = prm.q8_scales + static_cast<size_t>(tokens) * h_q;
     prm.out_table = page_table;
     prm.out_lens = page_seqlens;
     prm.status = device_status;
@@ -583,24 +624,16 @@ mla_status mla_select_pages(const void* q, int batch, int s_q, int h_q, int d_qk
     else
         e = dtype == MLA_FP16 ? launch_scores<512, true>(grid, st, prm) : launch_scores<512, false>(grid, st, prm);
     if (e != cudaSuccess) return MLA_ERR_CUDA;
+    const bool small = max_blocks_per_seq <= kSelectThreadsSmall * kSelectPerSmall;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(tokens));
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (max_blocks_per_seq <= kSelectThreadsSmall * kSelectPerSmall) {
-        cfg.blockDim = dim3(kSelectThreadsSmall);
+    programmatic_launch(cfg, attr, dim3(static_cast<unsigned>(tokens)), dim3(small ? kSelectThreadsSmall : kSelectThreadsLarge), 0, st);
+    if (small)
         e = cudaLaunchKernelEx(&cfg, mla_select_pages_kernel<kSelectThreadsSmall, kSelectPerSmall>, prm);
-    } else if (max_blocks_per_seq <= kSelectThreadsLarge * kSelectPerLarge) {
-        cfg.blockDim = dim3(kSelectThreadsLarge);
+    else if (max_blocks_per_seq <= kSelectThreadsLarge * kSelectPerLarge)
         e = cudaLaunchKernelEx(&cfg, mla_select_pages_kernel<kSelectThreadsLarge, kSelectPerLarge>, prm);
-    } else {
-        cfg.blockDim = dim3(kSelectThreadsLarge);
+    else
         e = cudaLaunchKernelEx(&cfg, mla_select_pages_kernel<kSelectThreadsLarge, 0>, prm);
-    }
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

@@ -227,7 +227,7 @@ PyObject* do_select(PyObject* const* a)
     const int max_blocks = as_int(table.size(1), "max_blocks");
     const int topn = int_arg(a[5], "topn"), first = int_arg(a[6], "n_first"), last = int_arg(a[7], "n_last");
     int32_t* status = status_of(a[9], dev);
-    const size_t bytes = mla_select_workspace_bytes(b, s_q, max_blocks);
+    const size_t bytes = mla_select_workspace_bytes(b, s_q, h_q, d_qk, max_blocks);
     if (bytes == 0) throw Refused("invalid or unsupported sizes for the selection");
     const c10::cuda::CUDAGuard guard(dev);
     const int64_t tokens = static_cast<int64_t>(b) * s_q;

@@ -82,5 +82,5 @@ def test_select_refuses(lib, over, code):
 
 def test_select_of_no_requests_is_a_no_op(lib):
     assert select(lib, batch=0, q=None) == 0
-    assert lib.mla_select_workspace_bytes(2, 3, 10) >= 2 * 3 * 10 * 4
-    assert lib.mla_select_workspace_bytes(2, 0, 10) == 0
+    assert lib.mla_select_workspace_bytes(2, 3, 16, 576, 10) >= 2 * 3 * (16 * 580 + 10 * 4)
+    assert lib.mla_select_workspace_bytes(2, 0, 16, 576, 10) == 0
