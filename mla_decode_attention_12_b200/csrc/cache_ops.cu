@@ -271,65 +271,61 @@ struct SummarizeParams {
     int batch, max_blocks, num_blocks, d;
 };
 
-// One half page (32 rows) per stage of a ring that one thread keeps full by bulk copies.
-constexpr int kSumPhases = 8;                            // threads that share a column group: 4 rows of a stage each
-constexpr int kSumRows = 32 / kSumPhases;
+// Half a page per stage of a ring that one thread keeps full by bulk copies.
+constexpr int kSumStageRows = 32;
+constexpr int kSumPhases = 4;                            // threads that share a column group: 8 rows of a stage each
+constexpr int kSumRows = kSumStageRows / kSumPhases;
 constexpr int kSumWorkers = 72 * kSumPhases;             // 72 groups of 8 columns
 constexpr int kSumThreads = kSumWorkers + 32;            // and the loader's warp
-constexpr int kSumChunk = 1024;                          // requests per prefix sum
-constexpr unsigned long long kSumTimeoutNs = 2000000000ull;
+constexpr int kSumChunk = 512;                           // requests per prefix sum
 
 template <bool kFp8>
 struct SumLayout {
-    static constexpr int kStageBytes = 32 * (kFp8 ? kFp8RowBytes : 1152);  // (narrower rows use less of it)
-    static constexpr int kStages = kFp8 ? 7 : 4;
-    static constexpr int kOffPart = kStages * kStageBytes;                 // [phases][8][73] doubles
-    static constexpr int kOffFirst = kOffPart + kSumPhases * 8 * 73 * 8;   // [kSumChunk] first page, [kSumChunk + 1] prefix
+    static constexpr int kStageBytes = kSumStageRows * (kFp8 ? kFp8RowBytes : 1152);  // (narrower rows use less of it)
+    static constexpr int kStages = kFp8 ? 4 : 2;
+    static constexpr int kOffPart = kStages * kStageBytes;                 // [2 phases][4][73] float2
+    static constexpr int kOffFirst = kOffPart + 2 * kSumPhases * 4 * 73 * 8;   // [kSumChunk] first page, [kSumChunk + 1] prefix
     static constexpr int kOffBar = kOffFirst + (2 * kSumChunk + 2) * 4;
     static constexpr int kOffPage = kOffBar + 2 * kStages * 8;             // page of each stage
     static constexpr int kBytes = kOffPage + kStages * 4 + 128;
 };
-static_assert(SumLayout<false>::kBytes <= 232448 && SumLayout<true>::kBytes <= 232448, "shared memory plan exceeds 227 KB");
+static_assert(2 * (SumLayout<false>::kBytes + 1280) <= 233472 && 2 * (SumLayout<true>::kBytes + 1280) <= 233472,
+              "two blocks of an SM share 228 KB");
+static_assert(kSumWorkers % 32 == 0 && 2 * kSumWorkers >= 576 && kSumRows >= 1, "whole warps, two columns a worker at the end");
 static_assert(SumLayout<false>::kStageBytes % 128 == 0 && SumLayout<true>::kStageBytes % 128 == 0 &&
                   SumLayout<false>::kOffBar % 8 == 0 && SumLayout<true>::kOffBar % 8 == 0, "alignment");
 
-// Exact sum of two floats: s = fl(a + b), and what was rounded away.
-__device__ __forceinline__ float two_sum(float a, float b, float& err)
-{
-    const float s = __fadd_rn(a, b);
-    const float bb = __fsub_rn(s, a);
-    err = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
-    return s;
-}
+// Sums of pairs of columns that keep what each addition rounds away: hi + lo carries about 48 bits.
+struct Sum2 {
+    float2 hi = {0.f, 0.f}, lo = {0.f, 0.f};
 
-// Bounded wait for a phase of an mbarrier.
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity)
-{
-    if (mbar_test_wait(bar, parity)) return true;
-    const uint64_t start = global_timer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (global_timer_ns() - start > kSumTimeoutNs) return false;
-    return true;
-}
+    __device__ __forceinline__ void add(float2 x)
+    {
+        const float2 s = fadd2(hi, x), b = fsub2(s, hi);
+        lo = fadd2(lo, fadd2(fsub2(hi, fsub2(s, b)), fsub2(x, b)));  // s + (that) == hi + x exactly
+        hi = s;
+    }
+};
 
 // Key of a page: the mean of its 64 rows, as 8-bit whole numbers and a scale.  Bound by reading
 // the page (73.7 KB of 16-bit rows).  The key's rounding must not depend on the order of the sum,
-// so the sum is kept to about 48 bits: rows are added in pairs (two_sum, 32 bits), the pairs'
-// sums in 64 bits and what they rounded away in 32; a conversion to 64 bits per value instead of
-// per pair would take as long as the reads (16 conversions per clock and SM).
-// One block per SM takes every gridDim-th of the list of completed pages, which all blocks derive
-// alike (prefix sums over requests).  The loader's thread looks the pages up and keeps the ring of
-// half pages full by bulk copies (a page's rows are contiguous), so that up to 147 KB are in flight
-// while earlier rows are added; thread (g, phase) adds columns [8 g, 8 g + 8) of 4 rows of a stage,
-// and the phases meet in shared memory once per page.
+// so each sum is a pair of floats of about 48 bits together, kept by packed additions (two columns
+// an instruction, seven per pair of values).
+// Two blocks per SM take every gridDim-th of the list of completed pages, which all blocks derive
+// alike (prefix sums over requests).  A block's loader thread looks the pages up and keeps a ring of
+// half pages full by bulk copies (a page's rows are contiguous); thread (g, phase) adds columns
+// [8 g, 8 g + 8) of 8 rows of a stage, and the phases meet in shared memory once per page.  126 MB of
+// pages: 33.8 us, two thirds of it the reads (a plain sum of as many bytes takes 31); 39.5 with one
+// block per SM and twice the ring, whose additions and page ends nothing overlaps; 35.6 with quarter
+// pages.
 template <bool kFp16, bool kFp8>
-__global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const SummarizeParams p)
+__global__ void __launch_bounds__(kSumThreads, 2) mla_summarize_kernel(const SummarizeParams p)
 {
     using L = SumLayout<kFp8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    // partial sum of column 8 g + k: part[phase][k][g] (rows of 73: neighbouring threads on other banks)
-    double(*part)[8][73] = reinterpret_cast<double(*)[8][73]>(smem + L::kOffPart);
+    // partial sums of columns 8 g + 2 k, + 1: part[2 phase][k][g] and what they rounded away: part[2 phase + 1][k][g]
+    float2(*part)[4][73] = reinterpret_cast<float2(*)[4][73]>(smem + L::kOffPart);
     int* first = reinterpret_cast<int*>(smem + L::kOffFirst);
     int* offset = first + kSumChunk;
     volatile int* page_of = reinterpret_cast<volatile int*>(smem + L::kOffPage);
@@ -404,15 +400,15 @@ __global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const Sum
                         if (p.status) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
                         page = -1;
                     }
-                    for (int half = 0; half < 2 && ok; ++half, advance()) {
-                        if (!(ok = wait_for(empty + 8 * stage, parity ^ 1))) break;
+                    for (int r = 0; r < kPage && ok; r += kSumStageRows, advance()) {
+                        if (!(ok = mbar_wait_bounded(empty + 8 * stage, parity ^ 1))) break;
                         page_of[stage] = page;
                         if (page < 0) {
                             mbar_arrive(full + 8 * stage);
                         } else {
-                            mbar_arrive_expect_tx(full + 8 * stage, 32 * stride);
+                            mbar_arrive_expect_tx(full + 8 * stage, kSumStageRows * stride);
                             bulk_load(s_base + stage * L::kStageBytes,
-                                      p.cache + (static_cast<size_t>(page) * kPage + 32 * half) * stride, 32 * stride,
+                                      p.cache + (static_cast<size_t>(page) * kPage + r) * stride, kSumStageRows * stride,
                                       full + 8 * stage);
                         }
                     }
@@ -421,56 +417,37 @@ __global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const Sum
             __syncwarp();
         } else {
             for (long long i = skip; i < total; i += gridDim.x) {
-                double acc[8];
-                float rest[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k] = 0.0, rest[k] = 0.f;
-                auto add_pair = [&](const float (&a)[8], const float (&b)[8]) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float e;
-                        acc[k] += static_cast<double>(two_sum(a[k], b[k], e));
-                        rest[k] += e;
-                    }
-                };
+                Sum2 acc[4];
                 int page = -1;
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half, advance()) {
-                    ok = ok && wait_for(full + 8 * stage, parity);
+                for (int r0 = 0; r0 < kPage; r0 += kSumStageRows, advance()) {
+                    ok = ok && mbar_wait_bounded(full + 8 * stage, parity);
                     page = ok ? page_of[stage] : -1;
                     const uint8_t* row = smem + stage * L::kStageBytes + kSumRows * phase * stride;
                     if (page >= 0 && 8 * g < p.d) {
                         if (kFp8 && g < kLatent / 8) {
 #pragma unroll
-                            for (int r = 0; r < kSumRows; r += 2) {
-                                float v[2][8];
+                            for (int r = 0; r < kSumRows; ++r) {
+                                const uint2 raw = *reinterpret_cast<const uint2*>(row + r * kFp8RowBytes + 8 * g);
+                                const float sc = *reinterpret_cast<const float*>(row + r * kFp8RowBytes + kFp8ScaleOff + 4 * (g / 16));
 #pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    const uint2 raw = *reinterpret_cast<const uint2*>(row + (r + q) * kFp8RowBytes + 8 * g);
-                                    const float sc =
-                                        *reinterpret_cast<const float*>(row + (r + q) * kFp8RowBytes + kFp8ScaleOff + 4 * (g / 16));
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const uint32_t w = k < 2 ? raw.x : raw.y;
-                                        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                                            static_cast<__nv_fp8x2_storage_t>(w >> (16 * (k & 1))), __NV_E4M3);
-                                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                                        const float2 b = unpack16<false>(pack16<false>(f.x * sc, f.y * sc));
-                                        v[q][2 * k] = b.x;
-                                        v[q][2 * k + 1] = b.y;
-                                    }
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t w = k < 2 ? raw.x : raw.y;
+                                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                                        static_cast<__nv_fp8x2_storage_t>(w >> (16 * (k & 1))), __NV_E4M3);
+                                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                                    acc[k].add(unpack16<false>(pack16<false>(f.x * sc, f.y * sc)));
                                 }
-                                add_pair(v[0], v[1]);
                             }
                         } else {
                             // 16-bit columns: a 16-bit row's, or an FP8 row's position columns
                             const uint8_t* col = row + (kFp8 ? kFp8RopeOff + 16 * (g - kLatent / 8) : 16 * g);
 #pragma unroll
-                            for (int r = 0; r < kSumRows; r += 2) {
-                                float v0[8], v1[8];
-                                unpack8<kFp16>(*reinterpret_cast<const uint4*>(col + r * stride), v0);
-                                unpack8<kFp16>(*reinterpret_cast<const uint4*>(col + (r + 1) * stride), v1);
-                                add_pair(v0, v1);
+                            for (int r = 0; r < kSumRows; ++r) {
+                                const uint4 raw = *reinterpret_cast<const uint4*>(col + r * stride);
+                                const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) acc[k].add(unpack16<kFp16>(w[k]));
                             }
                         }
                     }
@@ -479,19 +456,24 @@ __global__ void __launch_bounds__(kSumThreads, 1) mla_summarize_kernel(const Sum
                 }
                 if (page >= 0 && 8 * g < p.d)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) part[phase][k][g] = acc[k] + static_cast<double>(rest[k]);
+                    for (int k = 0; k < 4; ++k) {
+                        part[2 * phase][k][g] = acc[k].hi;
+                        part[2 * phase + 1][k][g] = acc[k].lo;
+                    }
                 named_barrier_sync(1, kSumWorkers);
                 // columns 2 tid, 2 tid + 1: the mean, rounded once to 32 bits
                 float m0 = 0.f, m1 = 0.f;
                 if (2 * tid < p.d) {
-                    double s0 = 0.0, s1 = 0.0;
+                    Sum2 sum;
+                    float2 rest = {0.f, 0.f};
 #pragma unroll
                     for (int q = 0; q < kSumPhases; ++q) {
-                        s0 += part[q][(2 * tid) & 7][tid >> 2];
-                        s1 += part[q][(2 * tid + 1) & 7][tid >> 2];
+                        sum.add(part[2 * q][tid & 3][tid >> 2]);
+                        rest = fadd2(rest, part[2 * q + 1][tid & 3][tid >> 2]);
                     }
-                    m0 = static_cast<float>(s0 * (1.0 / kPage));
-                    m1 = static_cast<float>(s1 * (1.0 / kPage));
+                    rest = fadd2(rest, sum.lo);
+                    m0 = __fmul_rn(__fadd_rn(sum.hi.x, rest.x), 1.0f / kPage);
+                    m1 = __fmul_rn(__fadd_rn(sum.hi.y, rest.y), 1.0f / kPage);
                 }
                 float mx = fmaxf(fabsf(m0), fabsf(m1));
 #pragma unroll
@@ -648,7 +630,7 @@ mla_status mla_summarize_pages(const void* kvcache, int num_blocks, int page_siz
     prm.num_blocks = num_blocks;
     prm.d = d_qk;
     const long long most = static_cast<long long>(batch) * max_blocks_per_seq;  // no more pages than that
-    const int grid = most < sms ? static_cast<int>(most) : sms;
+    const int grid = most < 2 * sms ? static_cast<int>(most) : 2 * sms;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = fp8 ? launch_summarize<false, true>(grid, st, prm)
                               : (dtype == MLA_FP16 ? launch_summarize<true, false>(grid, st, prm)

@@ -21,7 +21,6 @@ constexpr int kTile = 128;                          // pages per tile: the rows 
 constexpr int kMaxHeads = 128;                      // query heads: its columns (N), in groups of 32
 constexpr int kKeyBoxBytes = kTile * 64;            // 128 rows x 64 bytes, swizzled in 64-byte rows
 constexpr float kTinyQ = 1.17549435e-38f;           // 2^-126
-constexpr unsigned long long kScoreTimeoutNs = 2000000000ull;
 
 struct SelectParams {
     const uint8_t* q;           // [tokens, h_q, d] 16-bit
@@ -346,13 +345,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const
                 }
                 mma_commit(bar);
             }
-            bool done = mbar_test_wait(bar, i & 1);
-            if (!done) {
-                const uint64_t start = global_timer_ns();
-                while (!(done = mbar_try_wait(bar, i & 1)) && global_timer_ns() - start < kScoreTimeoutNs) {
-                }
-            }
-            ok = __syncthreads_and(done) != 0;
+            ok = __syncthreads_and(mbar_wait_bounded(bar, i & 1)) != 0;
             if (!ok) break;
             tc_fence_after();
             // Thread (lane quarter, column group): its page's maximum over 32 heads.
