@@ -159,7 +159,8 @@ enum BarSlot : int {
     kBarKCopied = 32,    // local, 2 K stages: the V copies out of the stage landed (own + peer's view)
     kBarQCopied = 34,    // both: a round of Q boxes copied from the Q buffer into tensor memory
     kBarVLand = 35,      // local, 2 V stages (FP8 cache): this CTA's V stage copies landed (bytes)
-    kBarCount = 37
+    kBarSRead = 37,      // leader, 8 warps (4 per CTA): a step's logits are in registers (two-page steps)
+    kBarCount = 38
 };
 
 // Position in a ring of kN stages: stage index and the parity of its current use.
@@ -432,6 +433,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 {
     static_assert(!kFp8 || (kRope && !kFp16), "the FP8 cache has d_qk = 576 and bfloat16 queries");
     static_assert(!kVarlen || (!kSparse && !kPadHeads), "ragged runs read a block table and have no padding heads");
+    // Ragged runs over a 16-bit cache take two pages per step of the softmax (see there).
+    constexpr bool kTwoPages = kVarlen && !kFp8;
     using L = Layout<kRope, kFp8>;
     constexpr int kNumThreads = kFp8 ? kThreadsFp8 : kThreads;
     extern __shared__ uint8_t smem_raw[];
@@ -495,6 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             mbar_init(bar(kBarPFull + s), 8);
             mbar_init(bar(kBarPvDone + s), 1);
         }
+        mbar_init(bar(kBarSRead), 8);
         mbar_init(bar(kBarOFull), 1);
         mbar_init(bar(kBarOFree), 8);
         mbar_init(bar(kBarDrain), 1);
@@ -1077,6 +1081,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     __syncwarp();
                     return true;
                 };
+                // Two-page steps: P V of step `si`, whose np pages start at page gp.
+                uint32_t si = 0;
+                auto issue_pv_step = [&](uint32_t step, uint32_t gp, int np, bool first) -> bool {
+                    if (!wwait(bar(kBarPFull), step & 1)) return false;
+                    if (first && !wwait(bar(kBarOFree), (k & 1) ^ 1)) return false;
+                    for (int u = 0; u < np; ++u) {
+                        const uint32_t vs = (gp + u) & 1;
+                        if (!wwait(bar(kBarVFull + vs), ((gp + u) >> 1) & 1)) return false;
+                        tc_fence_after();
+                        if (issuer) {
+                            TL_EV(kEvMmaPvGo);
+                            const uint64_t pd0 = p_desc + ((u * L::kPBytes) >> 4);
+                            const uint64_t vd0 = v_desc + ((vs * L::kVBytes) >> 4);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_ss_pair(tmem + kTmemO + 128 * i, pd0 + ((kk * 32) >> 4),
+                                                vd0 + ((2 * i * 8192 + kk * 2048) >> 4), idesc_pv,
+                                                (first && u == 0 && kk == 0) ? 0u : 1u);
+                            }
+                            mma_commit_pair(bar(kBarVEmpty + vs), both);
+                            if (u == np - 1) mma_commit_pair(bar(kBarPvDone), both);
+                        }
+                        __syncwarp();
+                    }
+                    return true;
+                };
                 Ring<L::kKStages> kring;
                 while (ok && chunks.next(vb, lo, hi)) {
                     const int n = hi - lo;
@@ -1099,6 +1131,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     }
                     if (!ok || !(ok = wwait(bar(kBarQFull), (3 * k + 2) & 1))) break;
                     if (issuer) TL_EV(kEvMmaQFull);
+                    if constexpr (kTwoPages) {
+                        for (int j = 0; j < n && ok; j += 2, ++si) {
+                            const int np = min(2, n - j);
+                            // the S buffers: the softmax has read the last step's logits
+                            if (!(ok = wwait(bar(kBarSRead), (si & 1) ^ 1))) break;
+                            for (int u = 0; u < np && ok; ++u, kring.advance()) {
+                                const uint32_t st = kring.stage;
+                                if (!(ok = wwait(bar(kBarKFull + st), kring.phase))) break;
+                                tc_fence_after();
+                                if (issuer) {
+                                    TL_EV(kEvMmaKFull);
+                                    const uint64_t kd0 = k_desc + ((st * L::kKBytes) >> 4);
+#pragma unroll
+                                    for (int ks = 0; ks < 4 * kQTmemBoxes; ++ks)
+                                        mma_ts_pair(tmem + kTmemS + 32 * u, tmem + kTmemQ + 8 * ks,
+                                                    kd0 + (((ks >> 2) * 4096 + (ks & 3) * 32) >> 4), idesc_qk, ks > 0 ? 1u : 0u);
+#pragma unroll
+                                    for (int ks = 4 * kQTmemBoxes; ks < L::kKSteps; ++ks) {
+                                        const int box = ks >> 2, sub = ks & 3;
+                                        mma_ss_pair(tmem + kTmemS + 32 * u, q_desc + (((box - kQTmemBoxes) * 8192 + sub * 32) >> 4),
+                                                    kd0 + ((box * 4096 + sub * 32) >> 4), idesc_qk, 1u);
+                                    }
+                                    mma_commit_pair(bar(kBarKEmpty + st), both);
+                                    if (u == np - 1) mma_commit_pair(bar(kBarSFull), both);
+                                    if (j + u == n - 1) mma_commit_pair(bar(kBarQFree), both);
+                                }
+                                __syncwarp();
+                            }
+                            if (ok && j > 0) ok = issue_pv_step(si - 1, g + j - 2, 2, j == 2);
+                        }
+                        if (ok) {
+                            const int last = (n - 1) & ~1;
+                            ok = issue_pv_step(si - 1, g + last, n - last, last == 0);
+                        }
+                    } else {
                     for (int j = 0; j < n && ok; ++j, kring.advance()) {
                         const uint32_t gp = g + j;
                         const uint32_t sb = gp & 1;
@@ -1128,6 +1195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                         if (j > 0) ok = issue_pv(gp - 1, j == 1);
                     }
                     if (ok) ok = issue_pv(g + n - 1, n == 1);
+                    }
                     if (ok && issuer) mma_commit_pair(bar(kBarOFull), both);
                     __syncwarp();
                     g += n;
@@ -1154,6 +1222,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         uint32_t pair_phase = 0;
         const uint32_t p_full_lead = lead_bar(kBarPFull);  // + 8 per P buffer
         const uint32_t o_free_lead = lead_bar(kBarOFree);
+        const uint32_t s_read_lead = lead_bar(kBarSRead);
+        uint32_t si = 0;  // steps so far (two-page steps)
         auto wwait = [&](uint32_t b_, uint32_t par) { return __all_sync(0xffffffffu, sync.wait(b_, par)); };
         auto q_row_ptr = [&](int qvb, bool& valid) {
             if constexpr (kVarlen) {
@@ -1242,6 +1312,138 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             };
             int sp_idx = (kSparse && n > 0) ? entry(lo) : -1;
 
+            if constexpr (kTwoPages) {
+                // Two pages per step.  One warp per scheduler runs this loop, so a step costs the latency of its
+                // chain (logits from tensor memory, maximum, exchange between the row's halves,
+                // exponentials, P through the async proxy), about 1.2 us for one page's 32 logits per
+                // thread: more than the page's products.  Two pages share the waits, the exchange and
+                // the fences, and the next two pages' Q K^T run meanwhile (their S buffers are free as soon as
+                // the logits are in registers).
+                for (int j = 0; j < n; j += 2, ++si) {
+                    const bool both_pages = j + 1 < n;
+                    if (j <= j_prefetch && j_prefetch < j + 2) {
+                        ChunkIter<kVarlen> peek = chunks;
+                        int pvb, plo, phi;
+                        while (peek.next(pvb, plo, phi))
+                            if (phi > plo) {
+                                prefetch_q_row(pvb);
+                                break;
+                            }
+                    }
+                    if (!(ok = wwait(bar(kBarSFull), si & 1))) break;
+                    if (t == 0) TL_EV(kEvSFull);
+                    tc_fence_after();
+                    float x[64];
+                    {
+                        uint32_t a[2][32];
+                        tmem_ld32(tmem + kTmemS + lane_base, a[0]);
+                        tmem_ld32(tmem + kTmemS + 32 + lane_base, a[1]);
+                        tmem_wait_ld();
+                        reg_fence(a[0]);
+                        reg_fence(a[1]);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (leader)
+                                mbar_arrive(bar(kBarSRead));
+                            else
+                                mbar_arrive_remote(s_read_lead);
+                        }
+                        const int lim = n_vis - (lo + j) * kPage - 32 * h;  // columns >= lim of the first page are not visible
+                        // (the second page's lie 64 further; without one, its buffer holds an older page's)
+                        const int lim1 = both_pages ? lim - kPage : 0;
+                        if (__all_sync(0xffffffffu, lim1 >= 32)) {
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(a[c >> 5][c & 31]);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 64; ++c)
+                                x[c] = (c & 31) < (c < 32 ? lim : lim1) ? __uint_as_float(a[c >> 5][c & 31]) : -INFINITY;
+                        }
+                    }
+                    float mx;
+                    {
+                        float m16[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) m16[c] = fmaxf(fmaxf(x[c], x[c + 16]), fmaxf(x[c + 32], x[c + 48]));
+#pragma unroll
+                        for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                            for (int c = 0; c < w; ++c) m16[c] = fmaxf(m16[c], m16[c + w]);
+                        mx = m16[0] * p.scale_log2;  // log2-domain maximum (-inf stays -inf)
+                    }
+                    const uint32_t rb = si & 1;
+                    red[rb * 128 + t] = mx;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pair_bar);
+                    if (!(ok = wwait(pair_bar, pair_phase++ & 1))) break;
+                    mx = fmaxf(mx, red[rb * 128 + (t ^ 64)]);
+                    row_max = fmaxf(row_max, mx);
+                    float alpha = 1.f;
+                    bool rescale = false;
+                    if (mx > m_ref + kRescaleThreshold) {
+                        if (m_ref != -INFINITY) {
+                            alpha = fast_exp2(m_ref - mx);
+                            rescale = (j > 0);
+                        }
+                        m_ref = mx;
+                    }
+                    const float ref = (m_ref == -INFINITY) ? 0.f : m_ref;
+                    uint32_t pk[32];
+                    float s16[16];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float p0 = fast_exp2(fmaf(x[2 * c], p.scale_log2, -ref));
+                        const float p1 = fast_exp2(fmaf(x[2 * c + 1], p.scale_log2, -ref));
+                        s16[c & 15] = c < 16 ? p0 + p1 : s16[c & 15] + (p0 + p1);
+                        pk[c] = pack2(p0, p1, kFp16);
+                    }
+#pragma unroll
+                    for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                        for (int c = 0; c < w; ++c) s16[c] += s16[c + w];
+                    l_half = l_half * alpha + s16[0];
+                    // The P buffers, and O before it is rescaled: the last step's P V is done.
+                    if (si > 0 && !(ok = wwait(bar(kBarPvDone), (si - 1) & 1))) break;
+                    if (__any_sync(0xffffffffu, rescale)) {
+                        tc_fence_after();
+                        const float a = rescale ? alpha : 1.f;
+#pragma unroll 1
+                        for (int cb = 0; cb < 8; ++cb) {
+                            uint32_t v[32];
+                            const uint32_t addr = tmem + kTmemO + lane_base + 32 * cb;
+                            tmem_ld32(addr, v);
+                            tmem_wait_ld();
+                            reg_fence(v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+                            tmem_st32(addr, v);
+                        }
+                        tmem_wait_st();
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (u == 1 && !both_pages) break;
+                        uint8_t* prow = smem + L::kOffP + u * L::kPBytes + r * 128;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int chunk = (4 * h + q) ^ (r & 7);
+                            *reinterpret_cast<uint4*>(prow + chunk * 16) = make_uint4(
+                                pk[16 * u + 4 * q], pk[16 * u + 4 * q + 1], pk[16 * u + 4 * q + 2], pk[16 * u + 4 * q + 3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader)
+                            mbar_arrive(bar(kBarPFull));
+                        else
+                            mbar_arrive_remote(p_full_lead);
+                    }
+                    if (t == 0) TL_EV(kEvPPosted);
+                }
+            } else {
             for (int j = 0; j < n; ++j) {
                 if (j == j_prefetch) {
                     ChunkIter<kVarlen> peek = chunks;
@@ -1369,6 +1571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                         mbar_arrive_remote(p_full_lead + 8u * sb);
                 }
                 if (t == 0) TL_EV(kEvPPosted);
+            }
             }
             if (!ok) break;
 
