@@ -344,11 +344,17 @@ MLA_API mla_status mla_sparse_prefill(const void* q, int s_q, int h_q, int d_qk,
  * mla_decode_varlen:
  *   q              device [total_q, h_q, d_qk], dtype `dtype`, 16-byte aligned
  *   kvcache, block_table, dv, dtype, softmax_scale   as for mla_decode_with_kvcache
+ *   cache_seqlens  the array given to mla_get_metadata_varlen
  *   plan, num_parts   from mla_get_metadata_varlen for the same batch, total_q and h_q
  *   o              device [total_q, h_q, 512], 16-byte aligned;  lse device float32 [total_q, h_q]
  *   workspace      >= mla_decode_varlen_workspace_bytes(num_parts), control block zero as for
  *                  mla_decode_with_kvcache (one workspace serves both)
- *   Enqueues the split-KV and the combine kernel on `stream`.
+ *   scratch        device, >= mla_decode_varlen_scratch_bytes(...), 256-byte aligned, any contents, or
+ *                  null.  Over an FP8 cache, runs of several groups read each page several times: with
+ *                  scratch their pages are dequantized once into it (the same values); without, at
+ *                  every read.  mla_decode_varlen_scratch_bytes is 0 where it would not pay (16-bit
+ *                  caches, fewer than three groups per run) or would exceed 8 GiB.
+ *   Enqueues the split-KV and the combine kernel on `stream` (and, with scratch, one before them).
  */
 MLA_API size_t mla_varlen_plan_ints(int batch, int total_q, int h_q, int h_kv, int num_parts);
 MLA_API mla_status mla_get_metadata_varlen(const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, int batch, int total_q,
@@ -358,10 +364,12 @@ MLA_API mla_status mla_get_metadata_varlen_host(const int32_t* cu_seqlens_q, con
                                                 int total_q, int h_q, int h_kv, int causal, int num_parts,
                                                 int is_fp8_kvcache, int32_t* plan);
 MLA_API size_t mla_decode_varlen_workspace_bytes(int num_parts);
+MLA_API size_t mla_decode_varlen_scratch_bytes(int batch, int total_q, int h_q, int max_blocks_per_seq, int dtype);
 MLA_API mla_status mla_decode_varlen(const void* q, int total_q, int h_q, int d_qk, const void* kvcache, int num_blocks,
                                      int page_size, int h_kv, const int32_t* block_table, int batch,
-                                     int max_blocks_per_seq, int dv, int dtype, const int32_t* plan, int num_parts,
-                                     float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                     int max_blocks_per_seq, const int32_t* cache_seqlens, int dv, int dtype,
+                                     const int32_t* plan, int num_parts, float softmax_scale, void* o, float* lse,
+                                     void* workspace, size_t workspace_bytes, void* scratch, size_t scratch_bytes,
                                      void* stream);
 
 /*

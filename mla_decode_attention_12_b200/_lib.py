@@ -67,9 +67,10 @@ SIGNATURES = {
     "mla_decode_varlen_workspace_bytes": ([_I], _SZ),
     "mla_decode_varlen": ([_P, _I, _I, _I,              # q, total_q, h_q, d_qk
                            _P, _I, _I, _I,              # kvcache, num_blocks, page_size, h_kv
-                           _P, _I, _I, _I, _I,          # block_table, batch, max_blocks, dv, dtype
+                           _P, _I, _I, _P, _I, _I,      # block_table, batch, max_blocks, seqlens, dv, dtype
                            _P, _I, _F,                  # plan, num_parts, scale
-                           _P, _P, _P, _SZ, _P], _I),   # o, lse, workspace, ws_bytes, stream
+                           _P, _P, _P, _SZ, _P, _SZ, _P], _I),  # o, lse, workspace, ws_bytes, scratch, its bytes, stream
+    "mla_decode_varlen_scratch_bytes": ([_I, _I, _I, _I, _I], _SZ),
     "mla_select_workspace_bytes": ([_I, _I, _I, _I, _I], _SZ),
     "mla_select_pages": ([_P, _I, _I, _I, _I, _I,       # q, batch, s_q, h_q, d_qk, dtype
                           _P, _P, _I, _P, _I, _P,       # page_keys, page_scales, num_blocks, block_table, max_blocks, seqlens

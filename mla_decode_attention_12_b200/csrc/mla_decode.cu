@@ -1901,6 +1901,75 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(const __grid_constant_
     if (blockIdx.x == 0 && blockIdx.y == 0) grid_dependency_wait();
 }
 
+// ------------------------------------------------------------------ FP8 rows as 16-bit ones
+// 16 e4m3 values (one 16-byte word) times `s` -> 16 bfloat16 values (two 16-byte words): e4m3 -> half
+// (exact) -> float32 (exact), one multiply by s, one rounding to bfloat16.
+__device__ __forceinline__ void dequantize16(const uint4 raw, const float s, uint4& lo, uint4& hi)
+{
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __half2_raw h =
+            __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+        const float2 v = fmul2(__half22float2(*reinterpret_cast<const __half2*>(&h)), make_float2(s, s));
+        o[i] = pack2(v.x, v.y, false);
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// The pages of every run, dequantized once into scratch pages of 576 bfloat16 columns (page j of run b
+// is scratch page b * max_blocks + j) with their block table.  Memory bound: 1.8 KB per row.  One
+// block per page: a warp takes 8 rows, lane l the latent columns [16 l, 16 l + 16) and position
+// columns 2 l, 2 l + 1 of each, four rows in flight.
+constexpr int kDequantThreads = 256;
+constexpr int kRow16 = 576 * 2;
+
+__global__ void __launch_bounds__(kDequantThreads) mla_dequantize_pages_kernel(const uint8_t* cache, const int32_t* block_table,
+                                                                               const int32_t* seqlens, int batch, int max_blocks,
+                                                                               int num_blocks, uint8_t* out, int32_t* out_table,
+                                                                               int* status)
+{
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long units = static_cast<long long>(batch) * max_blocks;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int b = static_cast<int>(u / max_blocks), j = static_cast<int>(u - static_cast<long long>(b) * max_blocks);
+        if (threadIdx.x == 0) out_table[u] = static_cast<int>(u);
+        if (j >= pages_of(seqlens[b])) continue;
+        int page = block_table[u];
+        if (page < 0 || page >= num_blocks) {
+            if (threadIdx.x == 0) atomicCAS(status, 0, MLA_ERR_DEVICE_CHECK);
+            page = 0;
+        }
+        const uint8_t* src = cache + (static_cast<size_t>(page) * kPage + 8 * warp) * kFp8Row;
+        uint8_t* dst = out + (static_cast<size_t>(u) * kPage + 8 * warp) * kRow16;
+#pragma unroll
+        for (int r0 = 0; r0 < 8; r0 += 4) {
+            uint4 raw[4];
+            float sc[4];
+            uint32_t rope[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint8_t* row = src + (r0 + r) * kFp8Row;
+                raw[r] = __ldg(reinterpret_cast<const uint4*>(row) + lane);
+                sc[r] = __ldg(reinterpret_cast<const float*>(row + 512) + (lane >> 3));
+                rope[r] = __ldg(reinterpret_cast<const uint32_t*>(row + 528) + lane);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                uint4 lo, hi;
+                dequantize16(raw[r], sc[r], lo, hi);
+                uint8_t* row = dst + (r0 + r) * kRow16;
+                const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                st_global_32B(row + 32 * lane, w, true);
+                reinterpret_cast<uint32_t*>(row + 1024)[lane] = rope[r];
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------------ metadata kernel
 // Exclusive prefix sum over n values held in shared memory, by one CTA.
 template <typename T>
@@ -2340,6 +2409,30 @@ static mla_status check_varlen(int batch, int total_q, int h_q, int h_kv, int nu
     return MLA_OK;
 }
 
+// Whether a ragged call over an FP8 cache dequantizes its pages first.  A page costs a group of 128 query
+// rows 1.57 us of a partition when its rows are dequantized on the way and 1.0 us when they are 16-bit
+// already (pieces of 8 prompts, 64 heads, 1.4k to 8k cached rows: 1003 us against 681 us), and dequantizing
+// it costs 19 ns of the whole GPU: worth it from 2.4 groups per run on.  Scratch is one 16-bit page per
+// block-table entry; calls that would need more than 8 GiB read the FP8 rows directly.
+static bool varlen_dequantizes(int batch, int total_q, int h_q)
+{
+    return static_cast<long long>(total_q) * h_q >= 3ll * kRowsPerGroup * batch;
+}
+
+static int varlen_fixed_cost(int is_fp8, int batch, int total_q, int h_q)
+{
+    return is_fp8 && !varlen_dequantizes(batch, total_q, h_q) ? kFixedCostFp8 : kFixedCost;
+}
+
+static size_t varlen_scratch_bytes(int batch, int total_q, int h_q, int max_blocks, int dtype)
+{
+    if (dtype != MLA_BF16_FP8KV || batch <= 0 || max_blocks <= 0) return 0;
+    if (!varlen_dequantizes(batch, total_q, h_q)) return 0;
+    const long long pages = static_cast<long long>(batch) * max_blocks;
+    const long long bytes = pages * (kPage * kRow16 + 4) + 1024;
+    return pages * kPage < (1ll << 31) && bytes <= (8ll << 30) ? static_cast<size_t>(bytes) : 0;
+}
+
 size_t mla_varlen_plan_ints(int batch, int total_q, int h_q, int h_kv, int num_parts)
 {
     if (check_varlen(batch, total_q, h_q, h_kv, num_parts) != MLA_OK) return 0;
@@ -2374,7 +2467,7 @@ mla_status mla_get_metadata_varlen(const int32_t* cu_seqlens_q, const int32_t* c
             return MLA_ERR_CUDA;
     }
     mla_metadata_varlen_kernel<<<1, kVarThreads, smem, static_cast<cudaStream_t>(stream)>>>(
-        cu_seqlens_q, cache_seqlens, batch, total_q, h_q, causal, num_parts, is_fp8_kvcache ? kFixedCostFp8 : kFixedCost,
+        cu_seqlens_q, cache_seqlens, batch, total_q, h_q, causal, num_parts, varlen_fixed_cost(is_fp8_kvcache, batch, total_q, h_q),
         plan, groups, c_global);
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
@@ -2389,10 +2482,16 @@ mla_status mla_get_metadata_varlen_host(const int32_t* cu_seqlens_q, const int32
         if (cu_seqlens_q[b] < 0 || cu_seqlens_q[b + 1] < cu_seqlens_q[b] || cu_seqlens_q[b + 1] > total_q || cache_seqlens[b] < 0)
             return MLA_ERR_INVALID_ARG;
     schedule_varlen_host(cu_seqlens_q, cache_seqlens, batch, h_q, causal != 0, num_parts,
-                         is_fp8_kvcache ? kFixedCostFp8 : kFixedCost, plan, plan + static_cast<size_t>(num_parts) * kMdInts,
+                         varlen_fixed_cost(is_fp8_kvcache, batch, total_q, h_q), plan,
+                         plan + static_cast<size_t>(num_parts) * kMdInts,
                          reinterpret_cast<long long*>(plan + static_cast<size_t>(num_parts) * kMdInts +
                                                       static_cast<size_t>(varlen_groups(batch, total_q, h_q)) * kVarInts));
     return MLA_OK;
+}
+
+size_t mla_decode_varlen_scratch_bytes(int batch, int total_q, int h_q, int max_blocks_per_seq, int dtype)
+{
+    return varlen_scratch_bytes(batch, total_q, h_q, max_blocks_per_seq, dtype);
 }
 
 size_t mla_decode_varlen_workspace_bytes(int num_parts)
@@ -2713,24 +2812,27 @@ mla_status mla_sparse_prefill(const void* q, int s_q, int h_q, int d_qk, const v
 }
 
 mla_status mla_decode_varlen(const void* q, int total_q, int h_q, int d_qk, const void* kvcache, int num_blocks,
-                             int page_size, int h_kv, const int32_t* block_table, int batch, int max_blocks_per_seq, int dv,
-                             int dtype, const int32_t* plan, int num_parts, float softmax_scale, void* o, float* lse,
-                             void* workspace, size_t workspace_bytes, void* stream)
+                             int page_size, int h_kv, const int32_t* block_table, int batch, int max_blocks_per_seq,
+                             const int32_t* cache_seqlens, int dv, int dtype, const int32_t* plan, int num_parts,
+                             float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes, void* scratch,
+                             size_t scratch_bytes, void* stream)
 {
     const mla_status s = check_varlen(batch, total_q, h_q, h_kv, num_parts);
     if (s != MLA_OK) return s;
     if (num_blocks <= 0 || max_blocks_per_seq <= 0) return MLA_ERR_INVALID_ARG;
     if (dtype != MLA_BF16 && dtype != MLA_FP16 && dtype != MLA_BF16_FP8KV) return MLA_ERR_INVALID_ARG;
-    const bool fp8 = dtype == MLA_BF16_FP8KV;
+    bool fp8 = dtype == MLA_BF16_FP8KV;
     if (page_size != kPage || (d_qk != 576 && d_qk != 512) || dv != kDv || (fp8 && d_qk != 576)) return MLA_ERR_UNSUPPORTED;
     if (static_cast<long long>(num_blocks) * kPage >= (1ll << 31)) return MLA_ERR_UNSUPPORTED;
     if (batch == 0 || total_q == 0) return MLA_OK;
-    if (!q || !kvcache || !block_table || !plan || !o || !lse || !workspace) return MLA_ERR_INVALID_ARG;
+    if (!q || !kvcache || !block_table || !cache_seqlens || !plan || !o || !lse || !workspace) return MLA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(kvcache) & 15) ||
         (reinterpret_cast<uintptr_t>(o) & 15) || (reinterpret_cast<uintptr_t>(plan) & 15) ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255))
+        (reinterpret_cast<uintptr_t>(workspace) & 255) || (reinterpret_cast<uintptr_t>(scratch) & 255))
         return MLA_ERR_INVALID_ARG;
     if (workspace_bytes < mla_decode_varlen_workspace_bytes(num_parts)) return MLA_ERR_WORKSPACE;
+    const size_t want_scratch = varlen_scratch_bytes(batch, total_q, h_q, max_blocks_per_seq, dtype);
+    if (scratch && scratch_bytes < want_scratch) return MLA_ERR_WORKSPACE;
     if (!(softmax_scale > 0.f)) softmax_scale = 1.0f / std::sqrt(static_cast<float>(d_qk));
     const int rows = total_q * h_q;
     DecodeParams prm{};
@@ -2755,13 +2857,33 @@ mla_status mla_decode_varlen(const void* q, int total_q, int h_q, int d_qk, cons
     prm.d_qk = d_qk;
     prm.num_parts = num_parts;
     workspace_pointers(workspace, 2 * static_cast<size_t>(num_parts), prm);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (scratch && want_scratch) {
+        // pages, then their block table
+        uint8_t* pages16 = static_cast<uint8_t*>(scratch);
+        const long long pages = static_cast<long long>(batch) * max_blocks_per_seq;
+        int32_t* table16 = reinterpret_cast<int32_t*>(pages16 + static_cast<size_t>(pages) * kPage * kRow16);
+        int sms = 0;
+        if (!sm_count(&sms)) return MLA_ERR_CUDA;
+        const int blocks = pages < 8ll * sms ? static_cast<int>(pages) : 8 * sms;
+        mla_dequantize_pages_kernel<<<blocks, kDequantThreads, 0, st>>>(static_cast<const uint8_t*>(kvcache), block_table,
+                                                                       cache_seqlens, batch, max_blocks_per_seq, num_blocks,
+                                                                       pages16, table16, prm.status);
+        if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+        fp8 = false;
+        kvcache = pages16;
+        num_blocks = static_cast<int>(pages);
+        prm.kvcache = pages16;
+        prm.block_table = table16;
+        prm.num_blocks = num_blocks;
+        prm.dtype = MLA_BF16;
+    }
     const CUtensorMapDataType dt = dtype == MLA_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t row_bytes = static_cast<uint64_t>(d_qk) * 2;
     CUtensorMap maps[kNumMaps];
     if (!encode_3d(&maps[0], q, dt, d_qk, rows, 1, row_bytes, row_bytes * rows, 64, prm.box_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_paged_kv(maps, kvcache, dt, d_qk, static_cast<uint64_t>(num_blocks) * kPage, fp8))
         return MLA_ERR_CUDA;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int grid = 2 * num_parts;
     cudaError_t e;
     if (fp8)

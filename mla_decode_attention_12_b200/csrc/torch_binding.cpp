@@ -305,12 +305,20 @@ PyObject* do_varlen(PyObject* const* a)
     } else {
         lse = at::empty({total_q, h_q}, q.options().dtype(at::kFloat));
     }
+    // FP8 pages that several groups read are dequantized once, into memory of this call alone
+    const size_t scratch_bytes = c.dtype != MLA_BF16_FP8KV ? 0
+        : mla_decode_varlen_scratch_bytes(static_cast<int>(batch), static_cast<int>(total_q), static_cast<int>(h_q),
+                                          as_int(table.size(1), "max_blocks"), c.dtype);
+    at::Tensor scratch;
+    if (scratch_bytes) scratch = at::empty({static_cast<int64_t>(scratch_bytes)}, c.t.options());
     int st = MLA_OK;
     if (batch != 0 && total_q != 0)
         st = mla_decode_varlen(q.data_ptr(), static_cast<int>(total_q), static_cast<int>(h_q), c.d_qk, c.t.data_ptr(), c.num_blocks, c.page,
-                               c.h_kv, table.data_ptr<int32_t>(), static_cast<int>(batch), as_int(table.size(1), "max_blocks"), dv, c.dtype,
+                               c.h_kv, table.data_ptr<int32_t>(), static_cast<int>(batch), as_int(table.size(1), "max_blocks"),
+                               lens.data_ptr<int32_t>(), dv, c.dtype,
                                plan.data_ptr<int32_t>(), parts, static_cast<float>(float_arg(a[8], "softmax_scale")), out.data_ptr(),
-                               lse.data_ptr<float>(), ws.data_ptr(), ws.numel() * ws.element_size(), stream_of(c.dev));
+                               lse.data_ptr<float>(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                               scratch_bytes ? scratch.data_ptr() : nullptr, scratch_bytes, stream_of(c.dev));
     return Py_BuildValue("(iNN)", st, THPVariable_Wrap(out), THPVariable_Wrap(lse));
 }
 

@@ -95,9 +95,10 @@ def test_without_causal_mask(kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
-def test_rows_that_no_group_sees_may_hold_nan(kind):
+@pytest.mark.parametrize("new", [[3, 1], [6, 4]])  # an FP8 cache: read directly, and dequantized first
+def test_rows_that_no_group_sees_may_hold_nan(kind, new):
     # 128 heads: one token per group; the rows of later tokens, the tails and unowned pages are poisoned
-    new, lens = [3, 1], [70, 100]
+    lens = [70, 100]
     s = make(kind, new, lens, 128, seed=7)
     clean = run(s)
     cache = s["cache"].clone()
@@ -118,7 +119,8 @@ def test_rows_that_no_group_sees_may_hold_nan(kind):
     row = int(s["table"][0, last // PAGE]) * PAGE + last % PAGE
     flat[row] = 0xFF if kind == "fp8" else float("nan")
     o, lse = run(s)
-    assert torch.equal(o[:2], clean[0][:2]) and torch.equal(lse[:2], clean[1][:2])
+    n = new[0] - 1
+    assert torch.equal(o[:n], clean[0][:n]) and torch.equal(lse[:n], clean[1][:n])
 
 
 def test_rows_behind_the_last_run_stay():
@@ -197,6 +199,45 @@ def test_bad_pages_and_long_lengths_are_recorded():
     s["seqlens"][1] = -3       # a length below zero is an empty cache
     s["lens"][1] = 0
     check(s, *run(s, workspace=ws, num_parts=74))
+    assert mla.read_device_status(ws) == 0
+
+
+def test_bad_pages_of_a_dequantized_cache():
+    s = make("fp8", [5, 9], [140, 260], 128, seed=21)
+    ws = torch.zeros(mla.varlen_workspace_bytes(74), dtype=torch.uint8, device="cuda")
+    good = s["table"].clone()
+    s["table"][0, 1] = -1
+    run(s, workspace=ws, num_parts=74)  # (its outputs are unspecified)
+    assert mla.read_device_status(ws) == 6
+    s["table"] = good
+    check(s, *run(s, workspace=ws, num_parts=74))
+    assert mla.read_device_status(ws) == 0
+
+
+def test_dequantized_pages_are_the_pages_read_directly():
+    # the same runs through the C entry point, with and without scratch
+    import ctypes
+
+    from mla_decode_attention_12_b200 import _lib
+    s = make("fp8", [5, 9, 20], [140, 2600, 999], 128, seed=22)
+    d = {k: v.cuda() for k, v in s.items() if isinstance(v, torch.Tensor)}
+    plan = mla.get_mla_metadata_varlen(d["cu"], d["seqlens"], 34, 128, is_fp8_kvcache=True)
+    ws = torch.zeros(mla.varlen_workspace_bytes(plan.num_parts), dtype=torch.uint8, device="cuda")
+    lib = _lib.load()
+    size = lib.mla_decode_varlen_scratch_bytes(3, 34, 128, d["table"].shape[1], 2)
+    assert size > 0
+    scratch = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    for sc in (scratch, None):
+        o = torch.empty(34, 128, DV, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(34, 128, device="cuda")
+        st = lib.mla_decode_varlen(
+            d["q"].data_ptr(), 34, 128, 576, d["cache"].data_ptr(), d["cache"].shape[0], 64, 1, d["table"].data_ptr(), 3,
+            d["table"].shape[1], d["seqlens"].data_ptr(), DV, 2, plan.data.data_ptr(), plan.num_parts, ctypes.c_float(0.0),
+            o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), None if sc is None else sc.data_ptr(), size,
+            torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        torch.cuda.synchronize()
+        check(s, o, lse)
     assert mla.read_device_status(ws) == 0
 
 

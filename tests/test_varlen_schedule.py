@@ -73,20 +73,30 @@ def test_visible_rows_of_a_group_row():
     (dict(table=None), 1), (dict(ws=None), 1), (dict(q=FAKE + 2), 1), (dict(o=FAKE + 8), 1), (dict(plan=FAKE + 4), 1),
     (dict(ws=FAKE + 16), 1), (dict(num_blocks=0), 1), (dict(max_blocks=0), 1), (dict(dtype=9), 1), (dict(parts=0), 1),
     (dict(page=32), 2), (dict(h_kv=2), 2), (dict(d_qk=192), 2), (dict(dv=256), 2), (dict(dtype=2, d_qk=512), 2),
-    (dict(batch=16385), 2), (dict(total_q=1 << 24), 2), (dict(ws_bytes=100), 3),
+    (dict(batch=16385), 2), (dict(total_q=1 << 24), 2), (dict(ws_bytes=100), 3), (dict(lens=None), 1),
+    (dict(dtype=2, total_q=99, scratch=FAKE, scratch_bytes=1000), 3), (dict(dtype=2, total_q=99, scratch=FAKE + 64, scratch_bytes=1 << 40), 1),
 ])
 def test_decode_refuses(lib, over, code):
     a = dict(q=FAKE, total_q=9, h_q=64, d_qk=576, kvcache=FAKE, num_blocks=8, page=64, h_kv=1, table=FAKE, batch=2,
-             max_blocks=4, dv=512, dtype=0, plan=FAKE, parts=74, scale=0.0, o=FAKE, lse=FAKE, ws=FAKE, ws_bytes=1 << 40,
-             stream=None)
+             max_blocks=4, lens=FAKE, dv=512, dtype=0, plan=FAKE, parts=74, scale=0.0, o=FAKE, lse=FAKE, ws=FAKE,
+             ws_bytes=1 << 40, scratch=None, scratch_bytes=0, stream=None)
     a.update(over)
     assert lib.mla_decode_varlen(*a.values()) == code
 
 
 def test_no_runs_or_tokens_is_a_no_op(lib):
     for batch, total in ((0, 0), (3, 0)):
-        assert lib.mla_decode_varlen(None, total, 64, 576, None, 8, 64, 1, None, batch, 4, 512, 0, None, 74, 0.0, None, None,
-                                     None, 0, None) == 0
+        assert lib.mla_decode_varlen(None, total, 64, 576, None, 8, 64, 1, None, batch, 4, None, 512, 0, None, 74, 0.0, None,
+                                     None, None, 0, None, 0, None) == 0
+
+
+def test_scratch_is_for_fp8_pages_that_several_groups_read(lib):
+    size = lib.mla_decode_varlen_scratch_bytes
+    assert size(2, 100, 64, 10, 0) == 0 and size(2, 100, 64, 10, 1) == 0
+    assert size(2, 100, 64, 10, 2) >= 2 * 10 * 64 * 1152
+    assert size(2, 11, 64, 10, 2) == 0   # 5.5 groups for two runs
+    assert size(2, 12, 64, 10, 2) > 0    # 6
+    assert size(64, 10 ** 5, 64, 2048, 2) == 0  # 9.7 GB
 
 
 def test_metadata_refuses(lib):
