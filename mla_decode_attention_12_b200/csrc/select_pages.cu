@@ -8,6 +8,7 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/mla_decode.h"
 #include "host_util.cuh"
@@ -83,7 +84,8 @@ __host__ __device__ constexpr uint32_t instr_desc_i8(int M, int N)
 // One warp per (token, head): s = max|q| / 127, q8 = q / s rounded to float32 and then to the nearest
 // whole number.  The product with the reciprocal is within 3 * 2^-24 of the rounded quotient, relative,
 // so at most 2.3e-5 off: it rounds to the same number unless it lies that close to the middle
-// between two.  A lane that has such a value (one in 500) divides all of its values instead.
+// between two.  Columns where a lane has such a value are divided (half of the largest value is one, 63.5:
+// with 8-bit significands most rows have some).
 // Rounding by adding 1.5 * 2^23: the low byte of the sum's pattern is the whole number.
 // A kernel of its own: the CTAs of the scoring kernel that share a token would otherwise each do this
 // again, which took longer than their reads.
@@ -116,31 +118,28 @@ __global__ void __launch_bounds__(kQuantThreads) mla_quantize_queries_kernel(con
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float s = fmaxf(m * (1.0f / 127.0f), kTinyQ), inv = __frcp_rn(s);
     uint32_t w[kPer];
-    bool close = !(s < 1.0e38f);  // not finite: the division's answers
+    uint32_t close = 0;  // pairs of columns with a value near the middle between two whole numbers
+    const float2 inv2 = make_float2(inv, inv), magic = make_float2(12582912.f, 12582912.f);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-        const float y0 = __fmul_rn(f[k].x, inv), y1 = __fmul_rn(f[k].y, inv);
-        const float t0 = __fadd_rn(y0, 12582912.f), t1 = __fadd_rn(y1, 12582912.f);
-        const float d0 = __fsub_rn(y0, __fsub_rn(t0, 12582912.f)), d1 = __fsub_rn(y1, __fsub_rn(t1, 12582912.f));
-        close |= fabsf(d0) > 0.49997f || fabsf(d1) > 0.49997f;
-        w[k] = __byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x0040);
+        const float2 y = fmul2(f[k], inv2), t = fadd2(y, magic), d = fsub2(y, fsub2(t, magic));
+        if (!(fmaxf(fabsf(d.x), fabsf(d.y)) <= 0.49997f)) close |= 1u << k;  // (or NaN)
+        w[k] = __byte_perm(__float_as_uint(t.x), __float_as_uint(t.y), 0x0040);
     }
-    if (close) {
-#pragma unroll 1
-        for (int k = 0; k < kPer; ++k) {
-            // (indexed at run time only here: read again instead of keeping the registers addressable)
-            const uint32_t raw = __ldg(src + 32 * k + lane);
-            float2 x;
-            if constexpr (kFp16)
-                x = __half22float2(*reinterpret_cast<const __half2*>(&raw));
-            else
-                x = make_float2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xffff0000u));
-            const int a = max(-127, min(127, divided(x.x, s))), b = max(-127, min(127, divided(x.y, s)));
-            reinterpret_cast<uint16_t*>(p.q8 + row * kD)[32 * k + lane] = static_cast<uint16_t>((a & 0xff) | ((b & 0xff) << 8));
-        }
-    } else {
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) reinterpret_cast<uint16_t*>(p.q8 + row * kD)[32 * k + lane] = static_cast<uint16_t>(w[k]);
+    for (int k = 0; k < kPer; ++k) reinterpret_cast<uint16_t*>(p.q8 + row * kD)[32 * k + lane] = static_cast<uint16_t>(w[k]);
+    if (!(s < 1.0e38f)) close = (1u << kPer) - 1u;  // a row with infinities or NaN: the division's answers
+    for (uint32_t todo = __reduce_or_sync(0xffffffffu, close); todo; todo &= todo - 1) {
+        const int k = __ffs(todo) - 1;
+        // (read again: registers cannot be indexed at run time)
+        const uint32_t raw = __ldg(src + 32 * k + lane);
+        float2 x;
+        if constexpr (kFp16)
+            x = __half22float2(*reinterpret_cast<const __half2*>(&raw));
+        else
+            x = make_float2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xffff0000u));
+        const int a = max(-127, min(127, divided(x.x, s))), b = max(-127, min(127, divided(x.y, s)));
+        reinterpret_cast<uint16_t*>(p.q8 + row * kD)[32 * k + lane] = static_cast<uint16_t>((a & 0xff) | ((b & 0xff) << 8));
     }
     if (lane == 0) p.q8_scales[row] = s;
 }
@@ -152,10 +151,9 @@ struct ScoreLayout {
     static constexpr int kTileBytes = kBoxes * kKeyBoxBytes;  // 73.7 KB at 576
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kTileBytes;                   // two stages
-    static constexpr int kOffRed = kOffK + 2 * kTileBytes;     // [4][128] floats: column groups' maxima
-    static constexpr int kOffPid = kOffRed + 4 * kTile * 4;    // [2][128] pages
-    static constexpr int kOffQs = kOffPid + 2 * kTile * 4;     // [128] head scales
-    static constexpr int kOffBar = kOffQs + kMaxHeads * 4;
+    static constexpr int kOffRed = kOffK + 2 * kTileBytes;     // [2][4][128] floats: column groups' maxima, by stage
+    static constexpr int kOffQs = kOffRed + 2 * 4 * kTile * 4; // [2][128] head scales, by token parity
+    static constexpr int kOffBar = kOffQs + 2 * kMaxHeads * 4;
     static constexpr int kBytes = kOffBar + 64 + 1024;
 };
 static_assert(ScoreLayout<576>::kBytes <= 232448, "shared memory plan exceeds 227 KB");
@@ -172,22 +170,31 @@ static_assert(ScoreLayout<576>::kTileBytes % 1024 == 0 && ScoreLayout<512>::kTil
 // 16-byte asynchronous copies into the swizzled K-major layout of the MMA, two tiles in flight (the
 // first while the queries are still being quantized: programmatic launch); the
 // MMA has the pages as rows (M = 128) and the heads as columns, so a thread of the epilogue owns a
-// page and takes the maximum over heads in its registers: no exchange between lanes.
+// page and takes the maximum over heads in its registers: no exchange between lanes.  A warp fetches the
+// same 8 rows of every tile (their pages looked up one tile ahead) and finishes those pages' scores.
+// 96 registers: the SM keeps room for a block of the quantizing kernel beside it.
+// Per tile: wait for its products, refill its stage, wait for the next tile's keys, start the next
+// products, and only then take this one's maxima, so that products and copies run meanwhile.
 template <int kD, bool kFp16>
-__global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const SelectParams p)
+__global__ void __maxnreg__(96) mla_score_pages_kernel(const SelectParams p)
 {
     using L = ScoreLayout<kD>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s_base = smem_addr(smem);
-    float(*red)[kTile] = reinterpret_cast<float(*)[kTile]>(smem + L::kOffRed);
-    int(*pid)[kTile] = reinterpret_cast<int(*)[kTile]>(smem + L::kOffPid);
-    float* qscale = reinterpret_cast<float*>(smem + L::kOffQs);
+    float(*red)[4][kTile] = reinterpret_cast<float(*)[4][kTile]>(smem + L::kOffRed);
+    float(*qscale)[kMaxHeads] = reinterpret_cast<float(*)[kMaxHeads]>(smem + L::kOffQs);
     const uint32_t bar = s_base + L::kOffBar;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 16);
     __shared__ int sh_token, sh_tile, warp_tot[kScoreThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_launch_dependents();
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+        sh_token = p.tokens;
+        sh_tile = 0;
+    }
 
     // ---- this CTA's run [t_lo, t_hi) of the line of tiles: total first, then the token t_lo falls into
     auto block_scan = [&](int x, int& total) {  // exclusive
@@ -209,144 +216,197 @@ __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const
         }
         return before + incl - x;
     };
-    if (tid == 0) {
-        mbar_init(bar, 1);
-        fence_mbar_init();
-        sh_token = p.tokens;
-        sh_tile = 0;
-    }
-    if (warp == 0) {
-        tmem_alloc(smem_addr(tmem_slot), 256);
-        tmem_relinquish();
-    }
-    int mine = 0;
-    for (int t = tid; t < p.tokens; t += kScoreThreads) {
+    int t_lo = 0, t_hi = 0;
+    auto cut = [&](int line) {
+        t_lo = static_cast<int>(static_cast<long long>(line) * blockIdx.x / gridDim.x);
+        t_hi = static_cast<int>(static_cast<long long>(line) * (blockIdx.x + 1) / gridDim.x);
+    };
+    auto tiles_at = [&](int t) {
         bool too_long;
-        mine += tiles_of(seen_by(p, t, &too_long));
+        const int n = tiles_of(seen_by(p, t, &too_long));
         if (too_long && blockIdx.x == 0 && p.status) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
-    }
-    int line;
-    block_scan(mine, line);
-    const int t_lo = static_cast<int>(static_cast<long long>(line) * blockIdx.x / gridDim.x);
-    const int t_hi = static_cast<int>(static_cast<long long>(line) * (blockIdx.x + 1) / gridDim.x);
-    for (int t0 = 0, base = 0; t0 < p.tokens && base <= t_lo; t0 += kScoreThreads) {
-        const int x = t0 + tid < p.tokens ? tiles_of(seen_by(p, t0 + tid)) : 0;
-        int total;
-        const int at = base + block_scan(x, total);
+        return n;
+    };
+    auto claim = [&](int t, int at, int x) {  // token t has tiles [at, at + x) of the line
         if (at <= t_lo && t_lo < at + x) {
-            sh_token = t0 + tid;
+            sh_token = t;
             sh_tile = t_lo - at;
         }
-        base += total;
+    };
+    if (p.tokens <= kScoreThreads) {
+        const int x = tid < p.tokens ? tiles_at(tid) : 0;
+        int line;
+        const int at = block_scan(x, line);
+        cut(line);
+        claim(tid, at, x);
+    } else {
+        int mine = 0;
+        for (int t = tid; t < p.tokens; t += kScoreThreads) mine += tiles_at(t);
+        int line;
+        block_scan(mine, line);
+        cut(line);
+        for (int t0 = 0, base = 0; t0 < p.tokens && base <= t_lo; t0 += kScoreThreads) {
+            const int x = t0 + tid < p.tokens ? tiles_of(seen_by(p, t0 + tid)) : 0;
+            int total;
+            const int at = base + block_scan(x, total);
+            claim(t0 + tid, at, x);
+            base += total;
+        }
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
     const int n_here = t_hi - t_lo;
+    uint32_t tmem = 0;
 
     // Position on the line: token, tile in it, pages that the token sees.
     struct Place {
         int token, tile, n;
     };
-    auto start_of = [&](int token, int tile) { return Place{token, tile, token < p.tokens ? seen_by(p, token) : 0}; };
     auto next_of = [&](Place a) {
         if (a.tile + 1 < tiles_of(a.n)) return Place{a.token, a.tile + 1, a.n};
         Place b{a.token + 1, 0, 0};
         while (b.token < p.tokens && (b.n = seen_by(p, b.token)) == 0) ++b.token;
         return b;
     };
-    // the page of row tid < 128 of a tile, or -1 past the token's pages
-    auto page_at = [&](const Place& a) {
-        const int j = a.tile * kTile + tid;
-        if (a.token >= p.tokens || j >= pages_of(a.n)) return -1;
-        int page = __ldg(p.block_table + static_cast<size_t>(a.token / p.s_q) * p.max_blocks + j);
-        if (page < 0 || page >= p.num_blocks) {
-            if (p.status) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
-            page = 0;
-        }
-        return page;
+    const int my_row = 8 * warp + (lane & 7);  // lanes 0-7: the row of a tile whose page this lane looks up
+    // Its block-table entry (kNoRow past the token's pages), read a tile before checked() looks at it, so
+    // that nothing waits for it; and the page: -1 for no row.
+    constexpr int kNoRow = -0x7fffffff - 1;
+    auto entry_at = [&](const Place& a) {
+        const int j = a.tile * kTile + my_row;
+        if (lane >= 8 || a.token >= p.tokens || j >= pages_of(a.n)) return kNoRow;
+        return __ldg(p.block_table + static_cast<size_t>(a.token / p.s_q) * p.max_blocks + j);
     };
-    auto load_tile = [&](int stage) {  // 16-byte words of the rows whose pages are in pid[stage]
+    auto checked = [&](int entry, const Place& a) {
+        if (lane >= 8 || a.token >= p.tokens || a.tile * kTile + my_row >= pages_of(a.n)) return -1;
+        if (entry < 0 || entry >= p.num_blocks) {
+            if (p.status) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
+            return 0;
+        }
+        return entry;
+    };
+    constexpr int kWords = kD / 16;  // 16-byte words of a row
+    // Word c of row r in a tile of 64-byte swizzled rows: word c % 4 of box c / 4 at (c % 4) ^ ((r / 2) % 4).
+    auto word_at = [](int r, int c) { return (c >> 2) * kKeyBoxBytes + r * 64 + (((c & 3) ^ ((r >> 1) & 3)) << 4); };
+    // An instruction copies 16 words of two rows: both rows' 64 bytes of a box fill one 128-byte line of
+    // shared memory (32 words of one row meet on half the banks, eight ways).
+    const int half_row = lane >> 4, half_word = lane & 15;
+    auto load_tile = [&](int stage, int page) {  // this warp's 8 rows; lane l < 8 gives the page of row l
         const uint32_t dst = s_base + L::kOffK + stage * L::kTileBytes;
-        constexpr int kWords = kD / 16;
 #pragma unroll
-        for (int k = 0; k < kTile * kWords / kScoreThreads; ++k) {
-            const int i = tid + k * kScoreThreads;
-            const int r = i / kWords, c = i - r * kWords;
-            const int page = pid[stage][r];
-            // 64-byte swizzled rows: word c % 4 of box c / 4 goes to word (c % 4) ^ ((r / 2) % 4)
-            cp_async16(dst + (c >> 2) * kKeyBoxBytes + r * 64 + (((c & 3) ^ ((r >> 1) & 3)) << 4),
-                       p.keys + static_cast<size_t>(max(page, 0)) * kD + 16 * c, page >= 0);
+        for (int k = 0; k < 8; k += 2) {
+            const int pg = __shfl_sync(0xffffffffu, page, k + half_row), r = 8 * warp + k + half_row;
+            const int8_t* src = p.keys + static_cast<size_t>(max(pg, 0)) * kD + 16 * half_word;
+            cp_async16(dst + word_at(r, half_word), src, pg >= 0);
+            cp_async16(dst + word_at(r, 16 + half_word), src + 256, pg >= 0);
+        }
+        if constexpr (kWords > 32) {  // the last 4 words of the 8 rows, one a lane
+            static_assert(kWords == 36 || kWords == 32, "four words left over");
+            const int pg = __shfl_sync(0xffffffffu, page, lane >> 2), c = 32 + (lane & 3);
+            cp_async16(dst + word_at(8 * warp + (lane >> 2), c), p.keys + static_cast<size_t>(max(pg, 0)) * kD + 16 * c, pg >= 0);
         }
         cp_async_commit();
     };
-    static_assert((kTile * (kD / 16)) % kScoreThreads == 0, "whole rounds of copies");
+    const int ncols = (p.h_q + 31) & ~31;
+    auto load_queries = [&](int token, int buf) {
+        // In the layout of the tiles, 8 rows a warp; rows past the last head are zero.
+        const int8_t* base = p.q8 + static_cast<size_t>(token) * p.h_q * kD;
+        if (8 * warp < ncols) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+                const int h = 8 * warp + k + half_row;
+                const int8_t* src = base + static_cast<size_t>(h < p.h_q ? h : 0) * kD + 16 * half_word;
+                cp_async16(s_base + L::kOffQ + word_at(h, half_word), src, h < p.h_q);
+                cp_async16(s_base + L::kOffQ + word_at(h, 16 + half_word), src + 256, h < p.h_q);
+            }
+            if constexpr (kWords > 32) {
+                const int h = 8 * warp + (lane >> 2), c = 32 + (lane & 3);
+                cp_async16(s_base + L::kOffQ + word_at(h, c), base + static_cast<size_t>(h < p.h_q ? h : 0) * kD + 16 * c, h < p.h_q);
+            }
+        }
+        if (tid < ncols) qscale[buf][tid] = tid < p.h_q ? __ldcg(p.q8_scales + static_cast<size_t>(token) * p.h_q + tid) : 0.f;
+        cp_async_commit();
+    };
+    const uint32_t idesc = instr_desc_i8(kTile, ncols);
+    const bool elected = elect_one();
+    const uint64_t q_desc = smem_desc(s_base + L::kOffQ, 16, 512, kLayoutSW64);
+    const uint64_t k_desc = smem_desc(s_base + L::kOffK, 16, 512, kLayoutSW64);
+    auto products = [&](auto stage_c) {
+        constexpr int kStage = decltype(stage_c)::value;  // addresses differ by constants only: quick to issue
+#pragma unroll
+        for (int ks = 0; ks < 2 * L::kBoxes; ++ks) {  // 32 columns per step
+            constexpr uint32_t kA = (kStage * L::kTileBytes) >> 4;
+            const uint32_t off = ((ks >> 1) * kKeyBoxBytes + (ks & 1) * 32) >> 4;
+            mma_i8_ss(tmem + 128 * kStage, k_desc + kA + off, q_desc + off, idesc, ks > 0 ? 1u : 0u);
+        }
+        mma_commit(bar);
+    };
+    auto start_products = [&](int stage) {  // one lane of warp 0
+        if (warp != 0) return;
+        if (stage == 0) {
+            if (elected) products(std::integral_constant<int, 0>{});
+        } else {
+            if (elected) products(std::integral_constant<int, 1>{});
+        }
+        __syncwarp();
+    };
 
     // (What is read before grid_dependency_wait was written before the quantizing kernel started.)
     bool ok = true;
     if (n_here > 0) {
-        Place cur = start_of(sh_token, sh_tile), nxt = next_of(cur);
-        float scale_cur = 0.f, scale_nxt = 0.f;
-        int pid_nxt = -1;
-        if (tid < kTile) {
-            const int page = page_at(cur);
-            pid[0][tid] = page;
-            scale_cur = page >= 0 ? __ldg(p.scales + page) : 0.f;
-            pid_nxt = n_here > 1 ? page_at(nxt) : -1;
+        const Place none{p.tokens, 0, 0};
+        Place cur{sh_token, sh_tile, seen_by(p, sh_token)}, nxt = n_here > 1 ? next_of(cur) : none;
+        Place after = n_here > 2 ? next_of(nxt) : none;
+        const int entry_cur = entry_at(cur), entry_nxt = entry_at(nxt);
+        int entry_after = entry_at(after);
+        const int page_cur = checked(entry_cur, cur);
+        load_tile(0, page_cur);
+        int page_nxt = checked(entry_nxt, nxt);
+        if (warp == 0) {  // (its latency behind the first copies)
+            tmem_alloc(smem_addr(tmem_slot), 256);
+            tmem_relinquish();
         }
-        __syncthreads();
-        load_tile(0);
+        float scale_cur = page_cur >= 0 ? __ldg(p.scales + page_cur) : 0.f;
         grid_dependency_wait();
-        int q_token = -1;
-        const int ncols = (p.h_q + 31) & ~31;
-        const uint32_t idesc = instr_desc_i8(kTile, ncols);
+        load_queries(cur.token, 0);
+        int qbuf = 0;
+        if (n_here > 1) {
+            load_tile(1, page_nxt);
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
+        }
+        fence_proxy_async_smem();  // this thread's copies, before the tensor core reads them
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+        start_products(0);
         for (int i = 0; i < n_here; ++i) {
             const int stage = i & 1;
-            if (q_token != cur.token) {
-                // The token's heads, in the layout of the tiles.  Rows past the last head are zero.
-                // (The earlier token's products are done: its last tile's scores are out.)
-                q_token = cur.token;
-                constexpr int kWords = kD / 16;
-                const int8_t* src = p.q8 + static_cast<size_t>(cur.token) * p.h_q * kD;
-                for (int w = tid; w < ncols * kWords; w += kScoreThreads) {
-                    const int h = w / kWords, c = w - h * kWords;
-                    cp_async16(s_base + L::kOffQ + (c >> 2) * kKeyBoxBytes + h * 64 + (((c & 3) ^ ((h >> 1) & 3)) << 4),
-                               src + (h < p.h_q ? 16 * w : 0), h < p.h_q);
-                }
-                if (tid < ncols) qscale[tid] = tid < p.h_q ? __ldcg(p.q8_scales + static_cast<size_t>(cur.token) * p.h_q + tid) : 0.f;
-                cp_async_commit();
-            }
-            // the next tile's copies, before this one's are awaited
-            if (i + 1 < n_here) {
-                const Place after = next_of(nxt);
-                if (tid < kTile) {
-                    pid[stage ^ 1][tid] = pid_nxt;
-                    scale_nxt = pid_nxt >= 0 ? __ldg(p.scales + pid_nxt) : 0.f;
-                    pid_nxt = i + 2 < n_here ? page_at(after) : -1;
-                }
-                __syncthreads();
-                load_tile(stage ^ 1);
+            const bool more = i + 1 < n_here;
+            const Place third = i + 3 < n_here ? next_of(after) : none;
+            const int entry_third = entry_at(third);
+            const int page_after = checked(entry_after, after);
+            const float scale_nxt = page_nxt >= 0 ? __ldg(p.scales + page_nxt) : 0.f;
+            ok = mbar_wait_bounded(bar, i & 1);
+            ok = __syncthreads_and(ok) != 0;  // (and the last tile's maxima are taken)
+            if (!ok) break;
+            const bool new_token = more && nxt.token != cur.token;
+            const int qb = qbuf;
+            if (new_token) load_queries(nxt.token, qbuf ^= 1);
+            if (i + 2 < n_here) {
+                load_tile(stage, page_after);
                 cp_async_wait<1>();
             } else {
                 cp_async_wait<0>();
             }
-            fence_proxy_async_smem();  // this thread's copies and stores, before the tensor core reads them
-            tc_fence_before();         // (and the epilogue's loads of the tile before last are done)
-            __syncthreads();
-            if (warp == 0 && elect_one()) {
+            if (more) {
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncthreads();
                 tc_fence_after();
-                const uint64_t a0 = smem_desc(s_base + L::kOffK + stage * L::kTileBytes, 16, 512, kLayoutSW64);
-                const uint64_t b0 = smem_desc(s_base + L::kOffQ, 16, 512, kLayoutSW64);
-#pragma unroll
-                for (int ks = 0; ks < 2 * L::kBoxes; ++ks) {  // 32 columns per step
-                    const uint32_t off = ((ks >> 1) * kKeyBoxBytes + (ks & 1) * 32) >> 4;
-                    mma_i8_ss(tmem + 128 * stage, a0 + off, b0 + off, idesc, ks > 0 ? 1u : 0u);
-                }
-                mma_commit(bar);
+                start_products(stage ^ 1);
             }
-            ok = __syncthreads_and(mbar_wait_bounded(bar, i & 1)) != 0;
-            if (!ok) break;
             tc_fence_after();
             // Thread (lane quarter, column group): its page's maximum over 32 heads.
             const int row = 32 * (warp & 3) + lane, cg = warp >> 2;
@@ -356,29 +416,43 @@ __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const
                 tmem_wait_ld();
                 reg_fence(v);
                 float m = -INFINITY;
+                const int real = p.h_q - 32 * cg;  // heads of this group
+                const float4* qs = reinterpret_cast<const float4*>(qscale[qb] + 32 * cg);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float x = __fmul_rn(static_cast<float>(static_cast<int>(v[c])), qscale[32 * cg + c]);
-                    if (32 * cg + c < p.h_q) m = fmaxf(m, x);
+                for (int c = 0; c < 32; c += 4) {
+                    const float4 q4 = qs[c / 4];
+                    const float x0 = __fmul_rn(static_cast<float>(static_cast<int>(v[c])), q4.x);
+                    const float x1 = __fmul_rn(static_cast<float>(static_cast<int>(v[c + 1])), q4.y);
+                    const float x2 = __fmul_rn(static_cast<float>(static_cast<int>(v[c + 2])), q4.z);
+                    const float x3 = __fmul_rn(static_cast<float>(static_cast<int>(v[c + 3])), q4.w);
+                    if (c + 4 <= real) {
+                        m = fmaxf(m, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
+                    } else {
+                        if (c < real) m = fmaxf(m, x0);
+                        if (c + 1 < real) m = fmaxf(m, x1);
+                        if (c + 2 < real) m = fmaxf(m, x2);
+                    }
                 }
-                red[cg][row] = m;
+                red[stage][cg][row] = m;
             }
+            tc_fence_before();
             __syncthreads();
-            if (tid < kTile) {
-                const int j = cur.tile * kTile + tid, n_pages = pages_of(cur.n);
-                float m = red[0][tid];
-                for (int c = 1; 32 * c < ncols; ++c) m = fmaxf(m, red[c][tid]);
+            if (lane < 8) {
+                const int j = cur.tile * kTile + my_row, n_pages = pages_of(cur.n);
+                float m = red[stage][0][my_row];
+                for (int c = 1; 32 * c < ncols; ++c) m = fmaxf(m, red[stage][c][my_row]);
                 float s = __fmul_rn(m, scale_cur);
                 // finite, so that nothing beats a page that is always in
                 s = s == s ? fminf(fmaxf(s, -FLT_MAX), FLT_MAX) : -FLT_MAX;
                 if (j < p.first || j >= n_pages - p.last) s = INFINITY;
                 if (j < n_pages) p.scores[static_cast<size_t>(cur.token) * p.max_blocks + j] = s;
-                scale_cur = scale_nxt;
             }
-            if (i + 1 < n_here) {
-                cur = nxt;
-                nxt = next_of(nxt);
-            }
+            cur = nxt;
+            nxt = after;
+            after = third;
+            scale_cur = scale_nxt;
+            page_nxt = page_after;
+            entry_after = entry_third;
         }
     }
     if (n_here <= 0) grid_dependency_wait();  // no CTA, and so not the grid, ends before the quantizing one
@@ -392,7 +466,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 0 && n_here > 0) {
         tc_fence_after();
         tmem_dealloc(tmem, 256);
     }
@@ -405,7 +479,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) mla_score_pages_kernel(const
 // [i * kPer, (i + 1) * kPer), so ranks by prefix sums give the pages in order and ties to the lower.
 // kPer 0: more pages than a CTA's registers hold, read again each round.
 constexpr int kSelectThreadsSmall = 256, kSelectPerSmall = 8;    // up to 2,048 pages
-constexpr int kSelectThreadsLarge = 1024, kSelectPerLarge = 16;  // up to 16,384
+constexpr int kSelectThreadsLarge = 1024, kSelectPerLarge = 8;   // up to 8,192
 
 template <int kThreads, int kPer>
 __global__ void __launch_bounds__(kThreads) mla_select_pages_kernel(const SelectParams p)
@@ -414,7 +488,8 @@ __global__ void __launch_bounds__(kThreads) mla_select_pages_kernel(const Select
     __shared__ int part[2][3][kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int t = blockIdx.x;
-    grid_dependency_wait();
+    // What the selection reads beside the scores is older than the quantizing kernel's start: it is
+    // fetched while the scores are still being computed.
     const int sees = seen_by(p, t);
     const int n = pages_of(sees);
     const int per = kPer > 0 ? kPer : (n + kThreads - 1) / kThreads;
@@ -422,6 +497,12 @@ __global__ void __launch_bounds__(kThreads) mla_select_pages_kernel(const Select
     const int32_t* table = p.block_table + static_cast<size_t>(t / p.s_q) * p.max_blocks;
     int32_t* out = p.out_table + static_cast<size_t>(t) * p.topn;
     const int keep = min(n, p.topn);
+    int32_t mine[kPer > 0 ? kPer : 1];  // this thread's pages
+    if constexpr (kPer > 0) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) mine[k] = tid * kPer + k < n ? __ldg(table + tid * kPer + k) : 0;
+    }
+    grid_dependency_wait();
     for (int i = keep + tid; i < p.topn; i += kThreads) out[i] = -1;
     if (tid == 0) p.out_lens[t] = n > 0 ? (keep - 1) * kPage + (sees - (n - 1) * kPage) : 0;
     if (n <= p.topn) {
@@ -446,20 +527,35 @@ __global__ void __launch_bounds__(kThreads) mla_select_pages_kernel(const Select
             return pattern(tid * per + k);
     };
     int buf = 0;
+    // Sums over the block.  With kPer the counts are at most 8,192: two share a word.
     auto sum3 = [&](int a, int b, int c, int& ta, int& tb, int& tc) {
-        a = __reduce_add_sync(0xffffffffu, a);
-        b = __reduce_add_sync(0xffffffffu, b);
-        c = __reduce_add_sync(0xffffffffu, c);
-        if (lane == 0) {
-            part[buf][0][warp] = a;
-            part[buf][1][warp] = b;
-            part[buf][2][warp] = c;
-        }
-        __syncthreads();
         const bool in = lane < kWarps;
-        ta = __reduce_add_sync(0xffffffffu, in ? part[buf][0][lane] : 0);
-        tb = __reduce_add_sync(0xffffffffu, in ? part[buf][1][lane] : 0);
-        tc = __reduce_add_sync(0xffffffffu, in ? part[buf][2][lane] : 0);
+        if constexpr (kPer > 0) {
+            const unsigned ab = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(a) | (static_cast<unsigned>(b) << 16));
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (lane == 0) {
+                part[buf][0][warp] = static_cast<int>(ab);
+                part[buf][1][warp] = c;
+            }
+            __syncthreads();
+            const unsigned t2 = __reduce_add_sync(0xffffffffu, in ? static_cast<unsigned>(part[buf][0][lane]) : 0u);
+            tc = __reduce_add_sync(0xffffffffu, in ? part[buf][1][lane] : 0);
+            ta = static_cast<int>(t2 & 0xffffu);
+            tb = static_cast<int>(t2 >> 16);
+        } else {
+            a = __reduce_add_sync(0xffffffffu, a);
+            b = __reduce_add_sync(0xffffffffu, b);
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (lane == 0) {
+                part[buf][0][warp] = a;
+                part[buf][1][warp] = b;
+                part[buf][2][warp] = c;
+            }
+            __syncthreads();
+            ta = __reduce_add_sync(0xffffffffu, in ? part[buf][0][lane] : 0);
+            tb = __reduce_add_sync(0xffffffffu, in ? part[buf][1][lane] : 0);
+            tc = __reduce_add_sync(0xffffffffu, in ? part[buf][2][lane] : 0);
+        }
         buf ^= 1;
     };
     uint32_t thr = 0;  // the largest pattern with at least topn scores at or above it
@@ -522,7 +618,12 @@ __global__ void __launch_bounds__(kThreads) mla_select_pages_kernel(const Select
         const uint32_t x = get(k);
         const bool in = x > thr || (x == thr && equal_before < room);
         equal_before += x == thr;
-        if (in) out[at++] = table[tid * per + k];
+        if (in) {
+            if constexpr (kPer > 0)
+                out[at++] = mine[k];
+            else
+                out[at++] = table[tid * per + k];
+        }
     }
 }
 
