@@ -2109,16 +2109,17 @@ __global__ void __launch_bounds__(kVarThreads) mla_metadata_varlen_kernel(const 
         const int v = v0 + tid;
         long long cost = 0;
         if (v < nv) {
-            int lo = 0, hi = batch - 1;  // the last run with first[run] <= v (runs without tokens share a first)
+            const int u = group_on_line(v, nv, num_parts);
+            int lo = 0, hi = batch - 1;  // the last run with first[run] <= u (runs without tokens share a first)
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (first[mid] <= v)
+                if (first[mid] <= u)
                     lo = mid;
                 else
                     hi = mid - 1;
             }
             __align__(16) int32_t gr[kVarInts];
-            fill_group(gr, lo, v - first[lo], cu[lo], cu[lo + 1], max(seqlens[lo], 0), h_q, causal != 0);
+            fill_group(gr, lo, u - first[lo], cu[lo], cu[lo + 1], max(seqlens[lo], 0), h_q, causal != 0);
             int4* dst = reinterpret_cast<int4*>(groups + static_cast<size_t>(kVarInts) * v);
             dst[0] = make_int4(gr[0], gr[1], gr[2], gr[3]);
             dst[1] = make_int4(gr[4], gr[5], gr[6], gr[7]);

@@ -63,7 +63,11 @@ constexpr int kMdInts = 8;
 
 // Ragged runs of query tokens (chunks of prompts beside decode steps): run b is the query tokens
 // [cu[b], cu[b + 1]), its rows (tokens x heads) are cut into groups of 128, and a group is a virtual
-// batch, numbered run by run.  One row of the group table per virtual batch:
+// batch.  On the cost line groups 0, P, 2 P, ... come first, then 1, P + 1, ... (P partitions, groups counted
+// run by run), so that at any time the partitions work on neighbouring groups, which read the same
+// pages: the second read hits L2.  (Run by run, a partition reads a run's pages once for each of its
+// groups, and all runs are open at once.  Same box, run by run against this order: four prompts' pieces
+// 4993 and 4820 us, eight over an FP8 cache 763 and 713, 32 runs of 14 groups over 8 MB each 1188 and 1153.)  One row of the group table per virtual batch, in line order:
 enum VarField : int {
     kVarReq = 0,     // the run (request)
     kVarRow0 = 1,    // its first query row in the call's total_q * h_q rows
@@ -74,6 +78,15 @@ enum VarField : int {
     kVarSplits = 6,  // partitions that share it
     kVarInts = 8
 };
+
+// Group (counted run by run) at place i of the line.
+MLA_HD inline int group_on_line(int i, int nv, int num_parts)
+{
+    const int q = nv / num_parts, longer = nv % num_parts;  // `longer` classes have q + 1 groups, the others q
+    const int head = longer * (q + 1);
+    if (i < head) return (i % (q + 1)) * num_parts + i / (q + 1);
+    return ((i - head) % q) * num_parts + longer + (i - head) / q;
+}
 
 // Visible rows of token `tok` (of the call's tokens) of a run of tokens [t0, t1) over len cached
 // rows: the causal mask is aligned to the bottom right.
@@ -201,14 +214,17 @@ inline void schedule_varlen_host(const int32_t* cu, const int32_t* seqlens, int 
                                  int F, int32_t* md, int32_t* groups, long long* C)
 {
     int nv = 0;
+    for (int b = 0; b < batch; ++b) nv += row_groups((cu[b + 1] - cu[b]) * h_q);
+    // C, until it holds the prefix sums: the place of each group on the line
+    for (int i = 0; i < nv; ++i) C[group_on_line(i, nv, num_parts)] = i;
+    for (int b = 0, v = 0; b < batch; ++b)
+        for (int g = 0; g < row_groups((cu[b + 1] - cu[b]) * h_q); ++g, ++v)
+            fill_group(groups + kVarInts * C[v], b, g, cu[b], cu[b + 1], seqlens[b], h_q, causal);
     long long total = 0;
-    for (int b = 0; b < batch; ++b)
-        for (int g = 0; g < row_groups((cu[b + 1] - cu[b]) * h_q); ++g, ++nv) {
-            int32_t* gr = groups + static_cast<long long>(kVarInts) * nv;
-            fill_group(gr, b, g, cu[b], cu[b + 1], seqlens[b], h_q, causal);
-            C[nv] = total;
-            total += pages_of(gr[kVarLimit]) + F;
-        }
+    for (int i = 0; i < nv; ++i) {
+        C[i] = total;
+        total += pages_of(groups[static_cast<long long>(kVarInts) * i + kVarLimit]) + F;
+    }
     for (int p = 0; p < num_parts; ++p) partition_range(p, num_parts, C, nullptr, nv, total, F, md + p * kMdInts);
     for (int p = 0; p < num_parts; ++p) {
         int32_t* m = md + p * kMdInts;

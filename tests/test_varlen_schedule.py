@@ -37,6 +37,7 @@ def test_every_page_once(new, lens, h_q, causal, parts):
     cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     md, groups = mla.get_mla_metadata_varlen_host(cu, lens, h_q, causal=causal, num_parts=parts)
     want = groups_by_hand(new, lens, h_q, causal)
+    want = [g for c in range(parts) for g in want[c::parts]]  # groups 0, P, 2 P, ..., then 1, P + 1, ...
     assert [tuple(int(v) for v in (g[0], g[1], g[2], g[3], g[5])) for g in groups] == want
     pages = [-(-g[3] // 64) for g in want]
     cover = [np.zeros(n, int) for n in pages]
