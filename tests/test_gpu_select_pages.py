@@ -172,6 +172,45 @@ def test_side_streams_at_once():
         assert np.array_equal(t.cpu().numpy(), want[0]) and np.array_equal(n.cpu().numpy(), want[1])
 
 
+def test_captured_sparse_decodes_replayed_at_once():
+    """Two graphs of flash_mla_page_sparse, captured on one stream and replayed on two."""
+    work = []
+    for seed, lens, heads in ((31, [64 * 60, 64 * 33 + 5], 128), (32, [64 * 500], 64)):
+        s = make(lens, 1, heads, seed=seed)
+        cache = random_cache("bf16", s["keys"].shape[0], 576, seed)
+        d = {k: v.cuda() for k, v in s.items()}
+        dc = cache.cuda()
+
+        def step(d=d, dc=dc):
+            return mla.flash_mla_page_sparse(d["q"], dc, d["table"], d["seqlens"], DV, d["keys"], d["scales"], 32)
+
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            res = step()
+        work.append((s, cache, graph, res, step))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for (_, _, graph, _, _), st in zip(work, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    u = HALF_STEP[torch.bfloat16]
+    for s, cache, _, (o, lse), _ in work:
+        t, n = expected(s, 32, 1, 1)
+        rows = cache_rows64(cache, False)
+        for b in range(len(n)):
+            i = torch.arange(int(n[b]))
+            kv = rows[torch.from_numpy(t[b]).long()[i // PAGE] * PAGE + i % PAGE]
+            q = s["q"][b, 0]
+            vis = torch.full((q.shape[0],), int(n[b]))
+            want, want_l = attend64(q, kv, vis, 576 ** -0.5)
+            size = torch.softmax(q.double() @ kv.T * 576 ** -0.5, -1) @ kv[:, :DV].abs()
+            assert ((o[b, 0].cpu().double() - want).abs() <= (u + 2.0 ** -12) * size + u * want.abs() * (1 + 2.0 ** -7)).all()
+            assert ((lse[b, 0].cpu().double() - want_l).abs() <= 2.0 ** -14 * (1 + want_l.abs())).all()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
 def test_a_serving_step(kind):
     """Append a prompt in two runs, attend it, keep the page keys, then decode over the chosen pages."""

@@ -133,6 +133,61 @@ def test_rows_behind_the_last_run_stay():
     assert (out[12:] == 7.0).all() and (lse[12:] == 5.0).all()
 
 
+def test_rows_before_the_first_run_stay():
+    s = make("bf16", [3, 9], [40, 300], 20, seed=30, extra_q=2)
+    s["q"] = torch.cat([s["q"][12:], s["q"][:12]])
+    s["cu"] += 2
+    out = torch.full((14, 20, DV), 7.0, dtype=torch.bfloat16, device="cuda")
+    o, lse = run(s, out=out)
+    assert (o[:2] == 7.0).all()
+    s["q"] = s["q"][2:]
+    check(s, o[2:], lse[2:])
+
+
+@pytest.mark.parametrize("new,lens", [([], []), ([0, 0], [5, 70]), ([0], [0])])
+def test_no_runs_or_no_tokens(new, lens):
+    s = make("bf16", new, lens, 16, seed=31)
+    s["table"] = s["table"].reshape(len(lens), -1) if lens else torch.zeros(0, 3, dtype=torch.int32)
+    o, lse = run(s)
+    assert o.shape == (0, 16, DV) and lse.shape == (0, 16)
+    if lens:  # and with rows of a padded batch behind them
+        s["q"] = torch.zeros(5, 16, 576, dtype=torch.bfloat16)
+        out = torch.full((5, 16, DV), 7.0, dtype=torch.bfloat16, device="cuda")
+        run(s, out=out)
+        assert (out == 7.0).all()
+
+
+@pytest.mark.parametrize("kind,new", [("bf16", [2, 3]), ("fp8", [1, 1]), ("fp8", [5, 7])])
+def test_pages_past_32_bit_offsets(kind, new):
+    # a cache of 4.3 GB and more: the byte offsets of its last pages pass 2^32
+    lens = [200, 65]
+    s = make(kind, new, lens, 128, seed=32)
+    pages = 60000 if kind == "bf16" else 110000
+    d = {k: v.cuda() for k, v in s.items() if isinstance(v, torch.Tensor)}
+    small = s["cache"]
+    d["cache"] = torch.empty(pages, *small.shape[1:], dtype=small.dtype, device="cuda")
+    d["cache"][pages - small.shape[0]:] = small.cuda()
+    d["table"] = torch.where(d["table"] >= 0, d["table"] + (pages - small.shape[0]), -1).to(torch.int32)
+    check(s, *run(s, dev=d))
+
+
+def test_a_plan_written_again():
+    s = make("bf16", [3, 30], [40, 300], 20, seed=33)
+    d = {k: v.cuda() for k, v in s.items() if isinstance(v, torch.Tensor)}
+    plan = mla.get_mla_metadata_varlen(d["cu"], d["seqlens"], 33, 20)
+    s["new"], s["lens"] = [13, 20], [64, 257]  # within the pages of the table
+    d["cu"].copy_(torch.tensor([0, 13, 33]))
+    d["seqlens"].copy_(torch.tensor(s["lens"]))
+    again = mla.get_mla_metadata_varlen(d["cu"], d["seqlens"], 33, 20, out=plan)
+    assert again.data is plan.data or again.data.data_ptr() == plan.data.data_ptr()
+    for _ in range(2):  # two layers with one plan
+        check(s, *run(s, dev=d, plan=again))
+    with pytest.raises(ValueError):
+        mla.get_mla_metadata_varlen(d["cu"], d["seqlens"], 33, 10, out=plan)
+    with pytest.raises(ValueError):
+        mla.get_mla_metadata_varlen(d["cu"], d["seqlens"], 33, 20, causal=False, out=plan)
+
+
 def test_same_as_the_dense_decode():
     # runs of equal length are what the dense decode computes
     s = make("bf16", [2] * 5, [500, 64, 129, 2, 1000], 64, seed=9)
