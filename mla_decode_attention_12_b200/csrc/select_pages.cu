@@ -257,14 +257,22 @@ __global__ void __maxnreg__(96) mla_score_pages_kernel(const SelectParams p)
     const int n_here = t_hi - t_lo;
     uint32_t tmem = 0;
 
-    // Position on the line: token, tile in it, pages that the token sees.
+    // Position on the line: token (p.tokens: none), first page of its tile, pages that the token sees, the
+    // token's row of the block table.
     struct Place {
-        int token, tile, n;
+        int token, j0, pages;
+        const int32_t* table;
     };
-    auto next_of = [&](Place a) {
-        if (a.tile + 1 < tiles_of(a.n)) return Place{a.token, a.tile + 1, a.n};
-        Place b{a.token + 1, 0, 0};
-        while (b.token < p.tokens && (b.n = seen_by(p, b.token)) == 0) ++b.token;
+    const Place none{p.tokens, 0, 0, nullptr};
+    auto place_of = [&](int token, int tile) {
+        if (token >= p.tokens) return none;
+        return Place{token, tile * kTile, pages_of(seen_by(p, token)),
+                     p.block_table + static_cast<size_t>(token / p.s_q) * p.max_blocks};
+    };
+    auto next_of = [&](const Place& a) {
+        if (a.j0 + kTile < a.pages) return Place{a.token, a.j0 + kTile, a.pages, a.table};
+        Place b = place_of(a.token + 1, 0);
+        while (b.token < p.tokens && b.pages == 0) b = place_of(b.token + 1, 0);
         return b;
     };
     const int my_row = 8 * warp + (lane & 7);  // lanes 0-7: the row of a tile whose page this lane looks up
@@ -272,12 +280,11 @@ __global__ void __maxnreg__(96) mla_score_pages_kernel(const SelectParams p)
     // that nothing waits for it; and the page: -1 for no row.
     constexpr int kNoRow = -0x7fffffff - 1;
     auto entry_at = [&](const Place& a) {
-        const int j = a.tile * kTile + my_row;
-        if (lane >= 8 || a.token >= p.tokens || j >= pages_of(a.n)) return kNoRow;
-        return __ldg(p.block_table + static_cast<size_t>(a.token / p.s_q) * p.max_blocks + j);
+        const int j = a.j0 + my_row;
+        return lane < 8 && j < a.pages ? __ldg(a.table + j) : kNoRow;
     };
     auto checked = [&](int entry, const Place& a) {
-        if (lane >= 8 || a.token >= p.tokens || a.tile * kTile + my_row >= pages_of(a.n)) return -1;
+        if (lane >= 8 || a.j0 + my_row >= a.pages) return -1;
         if (entry < 0 || entry >= p.num_blocks) {
             if (p.status) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
             return 0;
@@ -353,8 +360,7 @@ __global__ void __maxnreg__(96) mla_score_pages_kernel(const SelectParams p)
     // (What is read before grid_dependency_wait was written before the quantizing kernel started.)
     bool ok = true;
     if (n_here > 0) {
-        const Place none{p.tokens, 0, 0};
-        Place cur{sh_token, sh_tile, seen_by(p, sh_token)}, nxt = n_here > 1 ? next_of(cur) : none;
+        Place cur = place_of(sh_token, sh_tile), nxt = n_here > 1 ? next_of(cur) : none;
         Place after = n_here > 2 ? next_of(nxt) : none;
         const int entry_cur = entry_at(cur), entry_nxt = entry_at(nxt);
         int entry_after = entry_at(after);
@@ -438,7 +444,7 @@ __global__ void __maxnreg__(96) mla_score_pages_kernel(const SelectParams p)
             tc_fence_before();
             __syncthreads();
             if (lane < 8) {
-                const int j = cur.tile * kTile + my_row, n_pages = pages_of(cur.n);
+                const int j = cur.j0 + my_row, n_pages = cur.pages;
                 float m = red[stage][0][my_row];
                 for (int c = 1; 32 * c < ncols; ++c) m = fmaxf(m, red[stage][c][my_row]);
                 float s = __fmul_rn(m, scale_cur);
@@ -472,12 +478,15 @@ __global__ void __maxnreg__(96) mla_score_pages_kernel(const SelectParams p)
     }
 }
 
-// Selection: one CTA per token.  The topn-th largest score is found bit by bit, two bits of the
-// (order-preserving) 32-bit pattern per round: each round counts the scores at or above three
-// candidate thresholds, in registers and one exchange between warps; 16 rounds whatever the values,
-// where a histogram would serialise on scores that share their leading bits.  Thread i holds scores
-// [i * kPer, (i + 1) * kPer), so ranks by prefix sums give the pages in order and ties to the lower.
-// kPer 0: more pages than a CTA's registers hold, read again each round.
+// Selection: one CTA per token.  What is searched for is the topn-th largest score as an
+// order-preserving 32-bit pattern; the pages above it are in, and of those equal to it the first.
+// Up to 8,192 pages, in registers: the scores that compete are counted in 1,024 bins between the smallest
+// and the largest of them, a suffix sum finds the bin that the searched one is in, and the few scores
+// of that bin rank one another: 4 exchanges between warps, about 1 us.  Where a bin holds too many
+// (equal scores), and for more pages, two bits of the pattern a round: each counts the scores at or
+// above three candidates; 16 rounds, 4.1 us.
+// Thread i holds scores [i * kPer, (i + 1) * kPer), so prefix sums give the pages in order and ties to
+// the lower.  kPer 0: scores are read again each round.
 constexpr int kSelectThreadsSmall = 256, kSelectPerSmall = 8;    // up to 2,048 pages
 constexpr int kSelectThreadsLarge = 1024, kSelectPerLarge = 8;   // up to 8,192
 
@@ -559,7 +568,101 @@ __global__ void __launch_bounds__(kThreads) mla_select_pages_kernel(const Select
         buf ^= 1;
     };
     uint32_t thr = 0;  // the largest pattern with at least topn scores at or above it
-    for (int bit = 30; bit >= 0; bit -= 2) {
+    bool found = false;
+    if constexpr (kPer > 0) {
+        // Two 16-bit counts a word: such a block then fits beside one of the scoring kernel's, to start early.
+        constexpr int kBins = 1024, kEach = kBins / kThreads, kMostRanked = 128;
+        constexpr uint32_t kInf = 0xff800000u;  // pattern of the pages that are always in; no other has it
+        __shared__ uint32_t hist[kBins / 2];
+        auto count_of = [&](int b) { return static_cast<int>((hist[b >> 1] >> (16 * (b & 1))) & 0xffffu); };
+        __shared__ uint32_t ranked[kMostRanked];
+        __shared__ uint32_t sh_thr;
+        __shared__ int sh_bin, sh_need, sh_ranked;
+        auto value = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); };
+        uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (key[k] != 0u && key[k] != kInf) {
+                lo = min(lo, key[k]);
+                hi = max(hi, key[k]);
+            }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) {
+            part[0][0][warp] = static_cast<int>(lo);
+            part[0][1][warp] = static_cast<int>(hi);
+        }
+        for (int k = tid; k < kBins / 2; k += kThreads) hist[k] = 0;
+        if (tid == 0) sh_ranked = 0;
+        __syncthreads();
+        lo = __reduce_min_sync(0xffffffffu, lane < kWarps ? static_cast<uint32_t>(part[0][0][lane]) : 0xffffffffu);
+        hi = __reduce_max_sync(0xffffffffu, lane < kWarps ? static_cast<uint32_t>(part[0][1][lane]) : 0u);
+        const int need = p.topn - p.first - p.last;  // of the competing scores (n > topn: some compete)
+        // Halves, so that the range is finite.  Each step is monotonic, so a larger score is in no lower bin.
+        const float base = 0.5f * value(lo), width = 0.5f * value(hi) - base, inv = (kBins - 1) / width;
+        if (need == 0) {
+            thr = kInf;
+            found = true;
+        } else if (width > 0.f && inv < FLT_MAX && inv > 0.f) {  // (the same for every thread)
+            int bin[kPer];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const bool in = key[k] != 0u && key[k] != kInf;
+                bin[k] = in ? min(kBins - 1, static_cast<int>((0.5f * value(key[k]) - base) * inv)) : -1;
+                if (in) atomicAdd(&hist[bin[k] >> 1], 1u << (16 * (bin[k] & 1)));
+            }
+            __syncthreads();
+            // scores in this thread's bins and in the threads' above
+            int own = 0;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) own += count_of(tid * kEach + k);
+            int suffix = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_down_sync(0xffffffffu, suffix, o);
+                if (lane + o < 32) suffix += y;
+            }
+            if (lane == 0) part[1][0][warp] = suffix;
+            __syncthreads();
+            int more = 0;
+            for (int w = warp + 1; w < kWarps; ++w) more += part[1][0][w];
+            int above = more + suffix - own;  // in the bins above this thread's
+            if (above < need && need <= above + own) {
+#pragma unroll
+                for (int k = kEach - 1; k >= 0; --k) {
+                    const int c = count_of(tid * kEach + k);
+                    if (above < need && need <= above + c) {
+                        sh_bin = tid * kEach + k;
+                        sh_need = need - above;
+                    }
+                    above += c;
+                }
+            }
+            __syncthreads();
+            const int the_bin = sh_bin, rank = sh_need, many = count_of(the_bin);
+            if (many <= kMostRanked) {
+#pragma unroll
+                for (int k = 0; k < kPer; ++k)
+                    if (bin[k] == the_bin) ranked[atomicAdd(&sh_ranked, 1)] = key[k];
+                __syncthreads();
+                // the rank-th largest of them (equal ones give the same answer)
+                if (tid < many) {
+                    const uint32_t x = ranked[tid];
+                    int greater = 0, equal = 0;
+                    for (int c = 0; c < many; ++c) {
+                        greater += ranked[c] > x;
+                        equal += ranked[c] == x;
+                    }
+                    if (greater < rank && rank <= greater + equal) sh_thr = x;
+                }
+                __syncthreads();
+                thr = sh_thr;
+                found = true;
+            }
+        }
+        __syncthreads();  // part may be written again
+    }
+    for (int bit = 30; bit >= 0 && !found; bit -= 2) {
         const uint32_t c1 = thr | (1u << bit), c2 = thr | (2u << bit), c3 = thr | (3u << bit);
         int a = 0, b = 0, c = 0;
         if constexpr (kPer > 0) {

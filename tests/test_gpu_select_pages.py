@@ -103,6 +103,20 @@ def test_equal_scores_go_to_the_lower_page():
     check(s, 33, 1, 1)
 
 
+def test_scores_far_apart_and_close_together():
+    for outlier in (1e30, 3e38, 1e-30):  # all others share a few bins, or overflow both ways, or vanish
+        s = make([64 * 700, 64 * 3000], 1, 16, seed=13)
+        s["scales"][::97] = outlier
+        check(s, 50, 1, 2)
+    s = make([64 * 1500], 1, 4, seed=14)
+    s["keys"][:] = s["keys"][0]
+    s["scales"] = 1.0 + torch.arange(s["scales"].shape[0]) * 2.0 ** -23  # neighbours in float32
+    check(s, 40, 0, 1)
+    s["scales"][:] = 1e-45
+    check(s, 40, 3, 3)
+    check(s, 6, 3, 3)  # nothing competes
+
+
 def test_zero_queries_and_scores_that_are_not_finite():
     s = make([64 * 50], 1, 16, seed=8)
     s["q"][:] = 0
