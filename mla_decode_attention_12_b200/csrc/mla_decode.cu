@@ -2067,16 +2067,16 @@ static size_t metadata_smem_bytes(int nv, int num_parts)
     return static_cast<size_t>(nv) * (8 + 4 + 4) + static_cast<size_t>(num_parts) * 8 + 16;
 }
 
-// The schedule of ragged runs: one CTA of kVarThreads threads.  The group table is built in tiles of
+// The schedule of ragged runs: one CTA (256 threads up to 512 groups: its barriers cost less; else 1024).  The group table is built in tiles of
 // one group per thread (its run found by binary search in the runs' first groups), with the cost
 // prefix carried from tile to tile; then one thread per partition, as above.  Latency bound: once
-// per step, for every layer.  C: the prefix sums, in shared memory where they fit (a partition's
+// per step, for every layer; starts and lengths are read once, into shared memory (up to 4,096 runs).  C: the prefix sums, in shared memory where they fit (a partition's
 // binary searches then take about 0.1 us instead of several), else behind the table.
 // Runs that are not an ascending split of the tokens give an empty schedule whose md rows carry an
 // error (field 5), which the decode records.
-constexpr int kVarThreads = 1024;
-constexpr int kVarMaxRuns = 16384;
+constexpr int kVarMaxRuns = 16384, kVarCachedRuns = 4096;
 
+template <int kVarThreads>
 __global__ void __launch_bounds__(kVarThreads) mla_metadata_varlen_kernel(const int32_t* cu, const int32_t* seqlens,
                                                                           int batch, int total_q, int h_q, int causal,
                                                                           int num_parts, int fixed_cost, int32_t* md,
@@ -2089,12 +2089,22 @@ __global__ void __launch_bounds__(kVarThreads) mla_metadata_varlen_kernel(const 
     __shared__ int bad;
     int32_t* first = reinterpret_cast<int32_t*>(meta_smem);  // [batch + 1] first group of each run
     int32_t* begins = first + ((batch + 2) & ~1);              // [num_parts][2]
-    long long* C = c_global ? c_global : reinterpret_cast<long long*>(begins + 2 * num_parts);
+    int32_t* cached = begins + 2 * num_parts;                  // [batch + 1] starts, [batch + 1] lengths
+    const bool small = batch <= kVarCachedRuns;
+    long long* C = c_global ? c_global : reinterpret_cast<long long*>(cached + (small ? 2 * ((batch + 2) & ~1) : 0));
+    const int32_t* cu_s = small ? cached : cu;
+    const int32_t* len_s = small ? cached + ((batch + 2) & ~1) : seqlens;
     const int tid = threadIdx.x;
     if (tid == 0) bad = 0;
     __syncthreads();
     for (int b = tid; b < batch; b += kVarThreads) {
         const int t0 = cu[b], t1 = cu[b + 1];
+        if (small) {
+            const int len = seqlens[b];
+            cached[b] = t0;
+            if (b == batch - 1) cached[batch] = t1;
+            cached[((batch + 2) & ~1) + b] = len;
+        }
         const bool fine = t0 >= 0 && t1 >= t0 && t1 <= total_q;
         if (!fine) bad = 1;
         first[b] = fine ? row_groups((t1 - t0) * h_q) : 0;
@@ -2119,7 +2129,7 @@ __global__ void __launch_bounds__(kVarThreads) mla_metadata_varlen_kernel(const 
                     hi = mid - 1;
             }
             __align__(16) int32_t gr[kVarInts];
-            fill_group(gr, lo, u - first[lo], cu[lo], cu[lo + 1], max(seqlens[lo], 0), h_q, causal != 0);
+            fill_group(gr, lo, u - first[lo], cu_s[lo], cu_s[lo + 1], max(len_s[lo], 0), h_q, causal != 0);
             int4* dst = reinterpret_cast<int4*>(groups + static_cast<size_t>(kVarInts) * v);
             dst[0] = make_int4(gr[0], gr[1], gr[2], gr[3]);
             dst[1] = make_int4(gr[4], gr[5], gr[6], gr[7]);
@@ -2454,20 +2464,25 @@ mla_status mla_get_metadata_varlen(const int32_t* cu_seqlens_q, const int32_t* c
     int32_t* groups = plan + static_cast<size_t>(num_parts) * kMdInts;
     long long* c_global = reinterpret_cast<long long*>(groups + static_cast<size_t>(most) * kVarInts);
     constexpr size_t kMost = 200 * 1024;
-    size_t smem = (static_cast<size_t>(batch) + 2) * 4 + static_cast<size_t>(num_parts) * 8 + 16;
+    const size_t runs = (static_cast<size_t>(batch) + 2) & ~static_cast<size_t>(1);
+    size_t smem = runs * 4 * (batch <= kVarCachedRuns ? 3 : 1) + static_cast<size_t>(num_parts) * 8 + 16;
     if (smem + static_cast<size_t>(most) * 8 <= kMost) {
         smem += static_cast<size_t>(most) * 8;
         c_global = nullptr;
     }
+    const bool few = most <= 512 && batch <= 512;
+    auto kern = few ? mla_metadata_varlen_kernel<256> : mla_metadata_varlen_kernel<1024>;
     if (smem > 48 * 1024) {
         static PerDeviceOnce configured;
         if (configured.run([] {
-                return cudaFuncSetAttribute(mla_metadata_varlen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            kMost);
+                const cudaError_t e = cudaFuncSetAttribute(mla_metadata_varlen_kernel<256>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+                return e != cudaSuccess ? e : cudaFuncSetAttribute(mla_metadata_varlen_kernel<1024>,
+                                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
             }) != cudaSuccess)
             return MLA_ERR_CUDA;
     }
-    mla_metadata_varlen_kernel<<<1, kVarThreads, smem, static_cast<cudaStream_t>(stream)>>>(
+    kern<<<1, few ? 256 : 1024, smem, static_cast<cudaStream_t>(stream)>>>(
         cu_seqlens_q, cache_seqlens, batch, total_q, h_q, causal, num_parts, varlen_fixed_cost(is_fp8_kvcache, batch, total_q, h_q),
         plan, groups, c_global);
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
