@@ -40,6 +40,10 @@
 //   locally, the peer's over distributed shared memory), so every token row is dequantized
 //   once and the MMA, softmax and epilogue are those of the 16-bit cache.
 //
+// * Ragged runs of new tokens (the kVarlen instantiations): groups of 128 query rows with a table that says
+//   which request and rows they are and where their view ends; 16-bit caches take two pages per step of the
+//   softmax, FP8 pages that several groups read are dequantized once.
+//
 // Every mbarrier wait is bounded: after kWaitTimeoutNs the waiting thread sets
 // an abort flag (seen by both CTAs of the cluster) and MLA_ERR_TIMEOUT in the
 // workspace status word, and every role winds down and frees tensor memory.
