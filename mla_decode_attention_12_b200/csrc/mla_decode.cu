@@ -349,7 +349,7 @@ template <bool kVarlen>
 struct ChunkIter {
     int vb, blk, end_vb, end_blk, batch;
     const int32_t* seqlens;  // ragged runs: the group table
-    int const_len;  // the length of every request when seqlens is null
+    int const_len;  // the length of every request when seqlens is null (ragged runs: pages of a table row)
 
     __device__ bool next(int& out_vb, int& lo, int& hi)
     {
@@ -362,6 +362,10 @@ struct ChunkIter {
         out_vb = vb;
         lo = blk;
         hi = (vb == end_vb) ? end_blk : n;
+        if constexpr (kVarlen) {  // a length beyond the table (recorded) is not followed past it
+            lo = min(lo, const_len);
+            hi = min(hi, const_len);
+        }
         ++vb;
         blk = 0;
         return true;
@@ -542,7 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     const int32_t* md = p.md + part * kMdInts;
     if constexpr (kVarlen)  // a schedule of runs that do not split the tokens is empty and says why
         if (blockIdx.x == 0 && threadIdx.x == 0 && md[5] != 0) atomicCAS(p.status, 0, md[5]);
-    ChunkIter<kVarlen> chunks{md[0], md[1], md[2], md[3], p.batch, kVarlen ? p.vgroups : p.seqlens, p.topk};
+    ChunkIter<kVarlen> chunks{md[0], md[1], md[2], md[3], p.batch, kVarlen ? p.vgroups : p.seqlens, kVarlen ? p.max_blocks : p.topk};
     const int begin_vb = md[0];
     const int begin_split = md[4];
 
@@ -1286,6 +1290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                 row_valid = row < rg + gr[kVarRows];
                 n_vis = min(max(gr[kVarSeen] + row / p.h_q, 0), gr[kVarLen]);
                 nsplit = gr[kVarSplits];
+                if (t == 0 && pages_of(gr[kVarLimit]) > p.max_blocks) atomicCAS(p.status, 0, MLA_ERR_DEVICE_CHECK);
                 slot = 2 * static_cast<size_t>(part) + (split_idx > 0 ? 0 : 1);
             } else {
                 b = vb_request(vb, p.batch), rg = vb_group(vb, p.batch);

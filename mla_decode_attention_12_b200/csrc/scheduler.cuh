@@ -103,6 +103,7 @@ MLA_HD inline int clamp_seen(long long seen, int len)
 // Group g of run b = tokens [t0, t1): its row of the table (kVarSplits = 1).
 MLA_HD inline void fill_group(int32_t* gr, int b, int g, int t0, int t1, int len, int h_q, bool causal)
 {
+    if (len > (1 << 30)) len = 1 << 30;  // no cache holds as many rows; page counts stay in 32 bits
     const int row0 = t0 * h_q + g * kRowsPerGroup, end = t1 * h_q;
     const int rows = end - row0 < kRowsPerGroup ? end - row0 : kRowsPerGroup;
     const int seen = run_seen(t1, len, causal);

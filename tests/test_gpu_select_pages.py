@@ -72,6 +72,7 @@ def check(s, topn, first=1, last=1, causal=True):
 @pytest.mark.parametrize("lens,s_q,heads,topn,first,last", [
     ([1], 1, 1, 1, 0, 1), ([64 * 20], 1, 128, 5, 1, 1), ([64 * 200 + 3, 70, 0, 5000], 2, 16, 8, 1, 2),
     ([64 * 128, 64 * 129, 64 * 257 - 1], 1, 100, 16, 0, 3), ([3, 64 * 40], 4, 20, 4, 2, 2), ([9000] * 5, 1, 33, 64, 0, 1),
+    ([64 * 300 + 1, 64 * 7], 1, 96, 10, 1, 1),
 ])
 def test_choice(kind, d, lens, s_q, heads, topn, first, last):
     check(make(lens, s_q, heads, kind=kind, d=d, seed=len(lens) + heads), topn, first, last)

@@ -248,9 +248,10 @@ def test_bad_pages_and_long_lengths_are_recorded():
     assert mla.read_device_status(ws) == 6
     check(s, o, lse, only=[0])
     s["table"] = good
-    s["seqlens"][1] = 10 ** 5  # more pages than the table has
-    run(s, workspace=ws, num_parts=74)
-    assert mla.read_device_status(ws) == 6
+    for length in (10 ** 5, 2 ** 31 - 1):  # more pages than the table has: not followed past it
+        s["seqlens"][1] = length
+        run(s, workspace=ws, num_parts=74)
+        assert mla.read_device_status(ws) == 6
     s["seqlens"][1] = -3       # a length below zero is an empty cache
     s["lens"][1] = 0
     check(s, *run(s, workspace=ws, num_parts=74))
