@@ -84,3 +84,27 @@ def test_select_of_no_requests_is_a_no_op(lib):
     assert select(lib, batch=0, q=None) == 0
     assert lib.mla_select_workspace_bytes(2, 3, 16, 576, 10) >= 2 * 3 * (16 * 580 + 10 * 4)
     assert lib.mla_select_workspace_bytes(2, 0, 16, 576, 10) == 0
+
+
+def test_python_calls_refuse_host_tensors_and_other_things():
+    import torch
+
+    import mla_decode_attention_12_b200 as mla
+    i = torch.zeros(2, dtype=torch.int32)
+    table = torch.zeros(2, 3, dtype=torch.int32)
+    bf = torch.zeros(2, 64, 1, 576, dtype=torch.bfloat16)
+    keys, scales = torch.zeros(2, 576, dtype=torch.int8), torch.zeros(2)
+    calls = [
+        lambda: mla.mla_append_kvcache(bf[:, 0, 0, :512], bf[:, 0, 0, 512:], i, torch.zeros(4, 64), i, bf),
+        lambda: mla.mla_append_kvcache(None, None, None, None, None, None),
+        lambda: mla.mla_append_kvcache(bf[:, 0, 0, :512], None, None, None, "slots", bf),
+        lambda: mla.mla_summarize_pages(bf, table, i, i, keys, scales),
+        lambda: mla.mla_select_pages(bf[:, :1], keys, scales, table, i, 2),
+        lambda: mla.mla_select_pages(None, keys, scales, table, i, 2),
+        lambda: mla.get_mla_metadata_varlen(torch.zeros(3, dtype=torch.int32), i, 2, 16),
+        lambda: mla.flash_mla_varlen_with_kvcache(bf[:, 0], bf, table, torch.zeros(3, dtype=torch.int32), i, 512,
+                                                  mla.VarlenPlan(i, 2, 2, 1, 74, True)),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
