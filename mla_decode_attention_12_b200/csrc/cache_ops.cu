@@ -612,6 +612,8 @@ mla_status mla_summarize_pages(const void* kvcache, int num_blocks, int page_siz
     const bool fp8 = dtype == MLA_BF16_FP8KV;
     if (page_size != kPage || h_kv != 1 || (d_qk != 576 && d_qk != 512) || (fp8 && d_qk != 576)) return MLA_ERR_UNSUPPORTED;
     if (static_cast<long long>(num_blocks) * kPage >= (1ll << 31)) return MLA_ERR_UNSUPPORTED;
+    const long long most = static_cast<long long>(batch) * max_blocks_per_seq;  // pages that a step can complete: counted in int32
+    if (most >= (1ll << 31)) return MLA_ERR_UNSUPPORTED;
     if (batch == 0) return MLA_OK;
     if (!kvcache || !block_table || !prev_seqlens || !cache_seqlens || !page_keys || !page_scales) return MLA_ERR_INVALID_ARG;
     if (!aligned16(kvcache) || !aligned16(page_keys) || (reinterpret_cast<uintptr_t>(page_scales) & 3)) return MLA_ERR_INVALID_ARG;
@@ -629,7 +631,6 @@ mla_status mla_summarize_pages(const void* kvcache, int num_blocks, int page_siz
     prm.max_blocks = max_blocks_per_seq;
     prm.num_blocks = num_blocks;
     prm.d = d_qk;
-    const long long most = static_cast<long long>(batch) * max_blocks_per_seq;  // no more pages than that
     const int grid = most < 2 * sms ? static_cast<int>(most) : 2 * sms;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = fp8 ? launch_summarize<false, true>(grid, st, prm)

@@ -55,6 +55,11 @@ def test_summarize_refuses(lib, over, code):
     assert summarize(lib, **over) == code
 
 
+def test_summarize_refuses_a_table_whose_pages_pass_32_bits(lib):
+    assert summarize(lib, batch=512, max_blocks=1 << 22) == 2
+    assert summarize(lib, batch=2, max_blocks=1 << 30) == 2
+
+
 def test_summarize_of_no_requests_is_a_no_op(lib):
     assert summarize(lib, batch=0, kvcache=None) == 0
 
