@@ -149,11 +149,17 @@ MLA_API mla_status mla_get_metadata_host(const int32_t* cache_seqlens, int batch
  *
  * mla_decode_workspace_zero_bytes returns the size of the control block (the
  * same for every problem).  It must be zero before a workspace is first used;
- * every call that completes without a device error leaves it zero again, for
- * every later call of any size: the control block does not depend on the
- * problem, so the partial results of one call never land on the counters of
- * another.  After a device error (see mla_read_device_status, whose clear flag
- * zeroes the whole control block) zero it before reusing the workspace.
+ * every call leaves its counters zero again, for every later call of any size:
+ * the control block does not depend on the problem, so the partial results of
+ * one call never land on the counters of another.  The status word keeps the
+ * first device error until it is read with mla_read_device_status's clear flag;
+ * meanwhile the workspace serves further calls.  (The two stages of a call:
+ * the combine stage clears the counters.)
+ *
+ * Device errors.  MLA_ERR_DEVICE_CHECK: requests whose lengths and block-table
+ * entries are in order get their results, in this call too; what the others get
+ * is unspecified.  MLA_ERR_TIMEOUT: rows of the clusters whose wait gave up are
+ * not written, all others are.
  */
 #define MLA_MAX_VIRTUAL_BATCHES 16384
 MLA_API size_t mla_decode_workspace_bytes(int batch, int s_q, int h_q, int h_kv, int num_parts);
@@ -487,9 +493,9 @@ MLA_API mla_status mla_select_pages(const void* q, int batch, int s_q, int h_q, 
  * Reads the device status word of a workspace (synchronises `stream`).
  * *device_status receives MLA_OK or the first device-side error recorded by a
  * decode call that used this workspace; clear != 0 then zeroes the workspace's
- * whole control block (the status word back to MLA_OK, and the split / combine
- * counters a call that met a device error may have left nonzero), so the
- * workspace can be used again.
+ * whole control block (the status word back to MLA_OK; the split / combine
+ * counters are zero already after a whole call, but not after its first stage
+ * alone).
  */
 MLA_API mla_status mla_read_device_status(void* workspace, int clear, int* device_status, void* stream);
 

@@ -148,9 +148,9 @@ def get_workspace(nbytes: int, device: torch.device, zero_bytes: int) -> torch.T
     """A cached, grow-only workspace per (device, stream) whose control block is zero.
 
     ``zero_bytes`` is the control block's size (the same for every problem): it is
-    zeroed when the workspace is allocated, and every call that meets no device error
-    leaves it zero for the next call of any size.  ``read_device_status(ws, clear=True)``
-    zeroes it again after a device error.
+    zeroed when the workspace is allocated, and every call leaves its counters zero for the
+    next call of any size.  Its status word keeps the first device error until
+    ``read_device_status(ws, clear=True)``; calls go on working meanwhile.
     """
     key = (device.index, _stream(device))
     ws = _workspaces.get(key)
@@ -337,7 +337,7 @@ def read_device_status(workspace: torch.Tensor, clear: bool = True) -> int:
     """Device-side status recorded in a workspace (synchronises the current stream).
 
     ``clear`` zeroes the workspace's whole control block afterwards (status word and the
-    split / combine counters), so that it can be used again after a device error."""
+    split / combine counters)."""
     v = ctypes.c_int(0)
     dev = workspace.device
     with torch.cuda.device(dev):

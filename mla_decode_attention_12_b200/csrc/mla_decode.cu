@@ -105,6 +105,7 @@ constexpr int kQPrefetchPages = 8;         // pages before a chunk's end at whic
 #endif
 constexpr unsigned long long kWaitTimeoutNs = MLA_WAIT_TIMEOUT_NS;
 constexpr int kWorkspaceHeader = 256;
+constexpr int kSplitLost = 1 << 30;  // in the second counter of a virtual batch: one of its splits never came
 // The workspace's control block has room for the counters of this many virtual batches
 // (requests x row groups of 128 query rows), whatever the call: its size does not depend on
 // the problem, so the split partials of one call never overlap the counters of another.
@@ -1701,7 +1702,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             lo = nlo;
             hi = nhi;
         }
-        if (ok) announce();
+        announce();
+        // A warp whose wait gave up in chunk vb announces the splits it leaves all the same, marked as
+        // lost: every call's counters reach their full counts, so that the combine can clear them
+        // and no later call finds them half counted.
+        if (!ok && lane == 0) {
+            ChunkIter<kVarlen> rest{md[0], md[1], md[2], md[3], p.batch, kVarlen ? p.vgroups : p.seqlens,
+                                    kVarlen ? p.max_blocks : p.topk};
+            int left, left_lo, left_hi;
+            while (rest.next(left, left_lo, left_hi)) {
+                if (left < vb) continue;
+                const int idx = (left == begin_vb) ? begin_split : 0;
+                int at = left;
+                bool split;
+                if constexpr (kVarlen) {
+                    split = p.vgroups[kVarInts * left + kVarSplits] > 1;
+                    at = idx > 0 ? part - idx + 1 : part + 1;
+                } else {
+                    split = p.num_splits[left + 1] - p.num_splits[left] > 1;
+                }
+                if (!split) continue;
+                atomicOr(p.ctl + 2 * at + 1, kSplitLost);
+                __threadfence();
+                atomicAdd(p.ctl + 2 * at, 1);
+            }
+        }
         if (t == 0) TL_EV(kEvExit);
     }
 
@@ -1733,7 +1758,8 @@ __device__ __forceinline__ void combine_rows(const DecodeParams& p)
     // the wait below cannot starve its producers; it is bounded all the same.  The last
     // combine CTA of the virtual batch past the wait clears both counters for the next call.
     // (The schedule was written by the metadata grid, complete before the split-KV grid
-    // allowed this one to launch.)
+    // allowed this one to launch.)  A split that a cluster gave up is announced too, marked as lost:
+    // its virtual batch is not written, and its counters are cleared like the others.
     // blockIdx.x: the virtual batch, or, for ragged runs, the partition that holds its split 1 (at
     // most one split virtual batch starts its second split in a partition).
     int vb = blockIdx.x, slot0, nsplit, rows_here, row0 = 0;
@@ -1763,19 +1789,27 @@ __device__ __forceinline__ void combine_rows(const DecodeParams& p)
         while (!ready) {
             __nanosleep(200);
             ready = ld_acquire_gpu(split_done) >= want;
-            // A device error recorded by this call (a split-KV cluster that gave up, another
-            // combine CTA that timed out) means the splits may never all come: stop waiting.
-            if (!ready && ld_acquire_gpu(p.status) != 0) break;
-            if (!ready && global_timer_ns() - t0 > kWaitTimeoutNs) {
-                atomicCAS(p.status, 0, MLA_ERR_TIMEOUT);
+            // Where a wait gave up (this one, or one that the status word tells of, from this call or an
+            // earlier one), the end of the split-KV grid decides: its own waits are bounded, and each of its
+            // clusters announces all its splits, lost ones too, so that only a combine without its split-KV
+            // pass finds too few.  Other recorded errors (a block-table entry outside the cache, a length
+            // beyond the table) lose no split.
+            if (!ready && (global_timer_ns() - t0 > kWaitTimeoutNs || ld_acquire_gpu(p.status) == MLA_ERR_TIMEOUT)) {
+                grid_dependency_wait();
+                ready = ld_acquire_gpu(split_done) >= want;
+                if (!ready) atomicCAS(p.status, 0, MLA_ERR_TIMEOUT);
                 break;
             }
         }
-        if (ready && atomicAdd(combine_passed, 1) == static_cast<int>(gridDim.y) - 1) {
-            *combine_passed = 0;
-            *split_done = 0;
+        go = 0;
+        if (ready) {
+            const int passed = atomicAdd(combine_passed, 1);
+            if ((passed & ~kSplitLost) == static_cast<int>(gridDim.y) - 1) {
+                *combine_passed = 0;
+                *split_done = 0;
+            }
+            go = (passed & kSplitLost) == 0;  // rows that lost a split are not written
         }
-        go = ready;
     }
     __syncthreads();
     if (!go) return;
@@ -2246,8 +2280,8 @@ static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Workspace layout: a control block of fixed size (the status word, then two int32 counters
 // per virtual batch: split partials announced, combine CTAs past their wait), which must be
-// zero before the first call and is left zero by every call that completes without a device
-// error; then the split LSEs and the split partial outputs.  The control block's size does
+// zero before the first call; every call leaves the counters zero, and the status word too unless
+// it records a device error; then the split LSEs and the split partial outputs.  The control block's size does
 // not depend on the problem, so calls of different sizes can share one workspace.
 static void workspace_pointers(void* workspace, size_t slots, DecodeParams& prm)
 {
@@ -2944,7 +2978,7 @@ mla_status mla_read_device_status(void* workspace, int clear, int* device_status
         cudaStreamSynchronize(st) != cudaSuccess)
         return MLA_ERR_CUDA;
     *device_status = v;
-    // the whole control block: after a device error its counters may be left nonzero too
+    // the whole control block: a first stage whose combine never ran leaves counters too
     if (clear && cudaMemsetAsync(workspace, 0, kControlBytes, st) != cudaSuccess) return MLA_ERR_CUDA;
     return MLA_OK;
 }
@@ -3001,8 +3035,8 @@ extern "C" mla_status mla_decode_with_kvcache_noalloc(const void* q, int batch, 
     void* scratch = nullptr;
     mla_status st = noalloc_scratch(&scratch);
     if (st != MLA_OK) return st;
-    // The status word and this call's split / combine counters must start at zero (a call
-    // that met a device error may have left them nonzero); the split partials are always
+    // The status word and this call's split / combine counters must start at zero (an earlier
+    // call's error stays in the status word); the split partials are always
     // written before they are read, so the rest of the scratch needs no clearing.
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const size_t nv = static_cast<size_t>(batch) * row_groups(s_q * h_q / h_kv);
