@@ -211,6 +211,19 @@ MLA_API mla_status mla_decode_with_kvcache(const void* q, int batch, int s_q, in
                                    size_t workspace_bytes, void* stream);
 
 /*
+ * The same, with the call's device errors recorded in *device_status (device int32; the first error if it
+ * holds 0) instead of the workspace's status word; null: as mla_decode_with_kvcache.
+ */
+MLA_API mla_status mla_decode_with_kvcache_status(const void* q, int batch, int s_q, int h_q, int d_qk,
+                                   const void* kvcache, int num_blocks, int page_size, int h_kv,
+                                   const int32_t* block_table, int max_blocks_per_seq,
+                                   const int32_t* cache_seqlens, int dv, int dtype,
+                                   const int32_t* tile_md, int num_parts,
+                                   const int32_t* num_splits, int causal, float softmax_scale,
+                                   int active_heads, void* o, float* lse, void* workspace,
+                                   size_t workspace_bytes, int32_t* device_status, void* stream);
+
+/*
  * The two stages of mla_decode_with_kvcache, for callers that schedule or time
  * them separately (the split-KV / combine kernel pair named on the "FlashMLA
  * vLLM Optimization" page, background section).  Calling mla_decode_splitkv
@@ -361,6 +374,8 @@ MLA_API mla_status mla_sparse_prefill(const void* q, int s_q, int h_q, int d_qk,
  *                  every read.  mla_decode_varlen_scratch_bytes is 0 where it would not pay (16-bit
  *                  caches, fewer than three groups per run) or would exceed 8 GiB.
  *   Enqueues the split-KV and the combine kernel on `stream` (and, with scratch, one before them).
+ * mla_decode_varlen_status: the same, with the call's device errors recorded in *device_status (device int32; the
+ *   first error if it holds 0) instead of the workspace's status word; null: as mla_decode_varlen.
  */
 MLA_API size_t mla_varlen_plan_ints(int batch, int total_q, int h_q, int h_kv, int num_parts);
 MLA_API mla_status mla_get_metadata_varlen(const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, int batch, int total_q,
@@ -377,6 +392,12 @@ MLA_API mla_status mla_decode_varlen(const void* q, int total_q, int h_q, int d_
                                      const int32_t* plan, int num_parts, float softmax_scale, void* o, float* lse,
                                      void* workspace, size_t workspace_bytes, void* scratch, size_t scratch_bytes,
                                      void* stream);
+MLA_API mla_status mla_decode_varlen_status(const void* q, int total_q, int h_q, int d_qk, const void* kvcache,
+                                            int num_blocks, int page_size, int h_kv, const int32_t* block_table,
+                                            int batch, int max_blocks_per_seq, const int32_t* cache_seqlens, int dv,
+                                            int dtype, const int32_t* plan, int num_parts, float softmax_scale, void* o,
+                                            float* lse, void* workspace, size_t workspace_bytes, void* scratch,
+                                            size_t scratch_bytes, int32_t* device_status, void* stream);
 
 /*
  * Appending new tokens to the paged cache.  One pass over a step's new tokens: the latent is

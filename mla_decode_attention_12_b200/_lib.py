@@ -41,6 +41,8 @@ SIGNATURES = {
                                  _P, _I, _P, _I, _F,          # tile_md, num_parts, num_splits, causal, scale
                                  _I,                          # active_heads
                                  _P, _P, _P, _SZ, _P], _I),   # o, lse, workspace, ws_bytes, stream
+    "mla_decode_with_kvcache_status": ([_P, _I, _I, _I, _I, _P, _I, _I, _I, _P, _I, _P, _I, _I, _P, _I, _P, _I, _F, _I,
+                                        _P, _P, _P, _SZ, _P, _P], _I),  # the same, device_status before stream
     "mla_decode_splitkv": ([_P, _I, _I, _I, _I, _P, _I, _I, _I, _P, _I, _P, _I, _I,
                             _P, _I, _P, _I, _F, _I, _P, _P, _P, _SZ, _P], _I),
     "mla_decode_combine": ([_I, _I, _I, _I, _I, _I, _P, _I, _I, _P, _P, _P, _SZ, _P], _I),
@@ -70,6 +72,8 @@ SIGNATURES = {
                            _P, _I, _I, _P, _I, _I,      # block_table, batch, max_blocks, seqlens, dv, dtype
                            _P, _I, _F,                  # plan, num_parts, scale
                            _P, _P, _P, _SZ, _P, _SZ, _P], _I),  # o, lse, workspace, ws_bytes, scratch, its bytes, stream
+    "mla_decode_varlen_status": ([_P, _I, _I, _I, _P, _I, _I, _I, _P, _I, _I, _P, _I, _I, _P, _I, _F,
+                                  _P, _P, _P, _SZ, _P, _SZ, _P, _P], _I),  # the same, device_status before stream
     "mla_decode_varlen_scratch_bytes": ([_I, _I, _I, _I, _I], _SZ),
     "mla_select_workspace_bytes": ([_I, _I, _I, _I, _I], _SZ),
     "mla_select_pages": ([_P, _I, _I, _I, _I, _I,       # q, batch, s_q, h_q, d_qk, dtype

@@ -166,8 +166,11 @@ class DecodeCall:
 
     def __init__(self, q, kvcache, block_table, cache_seqlens, dv, tile_scheduler_metadata, num_splits,
                  causal=False, softmax_scale=None, workspace=None, out=None, lse=None, active_heads=None,
-                 is_fp8_kvcache=False, indices=None):
+                 is_fp8_kvcache=False, indices=None, status=None):
         dev = q.device
+        if status is not None and (indices is not None or status.dtype != torch.int32 or status.numel() != 1
+                                   or status.device != dev):
+            raise ValueError(f"status must be an int32 tensor of one value on {dev} (and is of the block-table decode)")
         self.sparse = indices is not None
         if self.sparse:
             if indices.dtype != torch.int32 or indices.dim() != 3 or indices.shape[:2] != q.shape[:2]:
@@ -209,7 +212,7 @@ class DecodeCall:
                                       workspace_zero_bytes(ws_b, ws_s, h_q, h_kv))
         scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(d_qk)
         self.device = dev
-        self.out, self.lse, self.workspace = out, lse, workspace
+        self.out, self.lse, self.workspace, self.status = out, lse, workspace, status
         self._keep = (q, kvcache, block_table, cache_seqlens, tile_scheduler_metadata, num_splits, indices)
         active = 0 if active_heads is None else int(active_heads)  # 0: every head is real
         dtype = MLA_BF16_FP8KV if is_fp8_kvcache else _DTYPES[q.dtype]
@@ -228,8 +231,11 @@ class DecodeCall:
     def run(self):
         """Split-KV kernel then combine kernel (mla_decode_with_kvcache / mla_decode_sparse)."""
         fn = "mla_decode_sparse" if self.sparse else "mla_decode_with_kvcache"
+        args = self.args
+        if self.status is not None:
+            fn, args = "mla_decode_with_kvcache_status", (*args, _ptr(self.status))
         with torch.cuda.device(self.device):
-            _lib.check(getattr(_lib.load(), fn)(*self.args, _stream(self.device)), fn)
+            _lib.check(getattr(_lib.load(), fn)(*args, _stream(self.device)), fn)
         return self.out, self.lse
 
     def splitkv(self):

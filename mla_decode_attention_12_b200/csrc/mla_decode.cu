@@ -2733,10 +2733,25 @@ mla_status mla_decode_with_kvcache(const void* q, int batch, int s_q, int h_q, i
                                    float softmax_scale, int active_heads, void* o, float* lse, void* workspace,
                                    size_t workspace_bytes, void* stream)
 {
+    return mla_decode_with_kvcache_status(q, batch, s_q, h_q, d_qk, kvcache, num_blocks, page_size, h_kv, block_table,
+                                          max_blocks_per_seq, cache_seqlens, dv, dtype, tile_md, num_parts, num_splits,
+                                          causal, softmax_scale, active_heads, o, lse, workspace, workspace_bytes, nullptr,
+                                          stream);
+}
+
+mla_status mla_decode_with_kvcache_status(const void* q, int batch, int s_q, int h_q, int d_qk, const void* kvcache,
+                                          int num_blocks, int page_size, int h_kv, const int32_t* block_table,
+                                          int max_blocks_per_seq, const int32_t* cache_seqlens, int dv, int dtype,
+                                          const int32_t* tile_md, int num_parts, const int32_t* num_splits, int causal,
+                                          float softmax_scale, int active_heads, void* o, float* lse, void* workspace,
+                                          size_t workspace_bytes, int32_t* device_status, void* stream)
+{
     DecodeParams prm;
     CUtensorMap maps[kNumMaps];
+    if (reinterpret_cast<uintptr_t>(device_status) & 3) return MLA_ERR_INVALID_ARG;
     mla_status s = prepare_decode(MLA_DECODE_ARGS, prm, maps);
     if (s != MLA_OK || batch == 0) return s;
+    if (device_status) prm.status = device_status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     s = launch_splitkv_stage(prm, maps, st);
     if (s != MLA_OK) return s;
@@ -2876,6 +2891,17 @@ mla_status mla_decode_varlen(const void* q, int total_q, int h_q, int d_qk, cons
                              float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes, void* scratch,
                              size_t scratch_bytes, void* stream)
 {
+    return mla_decode_varlen_status(q, total_q, h_q, d_qk, kvcache, num_blocks, page_size, h_kv, block_table, batch,
+                                    max_blocks_per_seq, cache_seqlens, dv, dtype, plan, num_parts, softmax_scale, o, lse,
+                                    workspace, workspace_bytes, scratch, scratch_bytes, nullptr, stream);
+}
+
+mla_status mla_decode_varlen_status(const void* q, int total_q, int h_q, int d_qk, const void* kvcache, int num_blocks,
+                                    int page_size, int h_kv, const int32_t* block_table, int batch, int max_blocks_per_seq,
+                                    const int32_t* cache_seqlens, int dv, int dtype, const int32_t* plan, int num_parts,
+                                    float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                    void* scratch, size_t scratch_bytes, int32_t* device_status, void* stream)
+{
     const mla_status s = check_varlen(batch, total_q, h_q, h_kv, num_parts);
     if (s != MLA_OK) return s;
     if (num_blocks <= 0 || max_blocks_per_seq <= 0) return MLA_ERR_INVALID_ARG;
@@ -2887,7 +2913,8 @@ mla_status mla_decode_varlen(const void* q, int total_q, int h_q, int d_qk, cons
     if (!q || !kvcache || !block_table || !cache_seqlens || !plan || !o || !lse || !workspace) return MLA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(kvcache) & 15) ||
         (reinterpret_cast<uintptr_t>(o) & 15) || (reinterpret_cast<uintptr_t>(plan) & 15) ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255) || (reinterpret_cast<uintptr_t>(scratch) & 255))
+        (reinterpret_cast<uintptr_t>(workspace) & 255) || (reinterpret_cast<uintptr_t>(scratch) & 255) ||
+        (reinterpret_cast<uintptr_t>(device_status) & 3))
         return MLA_ERR_INVALID_ARG;
     if (workspace_bytes < mla_decode_varlen_workspace_bytes(num_parts)) return MLA_ERR_WORKSPACE;
     const size_t want_scratch = varlen_scratch_bytes(batch, total_q, h_q, max_blocks_per_seq, dtype);
@@ -2916,6 +2943,7 @@ mla_status mla_decode_varlen(const void* q, int total_q, int h_q, int d_qk, cons
     prm.d_qk = d_qk;
     prm.num_parts = num_parts;
     workspace_pointers(workspace, 2 * static_cast<size_t>(num_parts), prm);
+    if (device_status) prm.status = device_status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (scratch && want_scratch) {
         // pages, then their block table

@@ -272,7 +272,7 @@ PyObject* do_varlen_plan(PyObject* const* a)
     return Py_BuildValue("(iiN)", st, parts, THPVariable_Wrap(plan));
 }
 
-// varlen(q, kvcache, block_table, cu_seqlens_q, cache_seqlens, dv, plan, num_parts, softmax_scale, fp8, workspace, out, lse)
+// varlen(q, kvcache, block_table, cu_seqlens_q, cache_seqlens, dv, plan, num_parts, softmax_scale, fp8, workspace, out, lse, status)
 //   -> (status, out, lse)
 PyObject* do_varlen(PyObject* const* a)
 {
@@ -290,6 +290,7 @@ PyObject* do_varlen(PyObject* const* a)
     const size_t ints = mla_varlen_plan_ints(as_int(batch, "batch"), as_int(total_q, "total_q"), as_int(h_q, "h_q"), c.h_kv, parts);
     if (ints == 0) return Py_BuildValue("(iOO)", MLA_ERR_UNSUPPORTED, Py_None, Py_None);
     need(plan, "plan", at::kInt, {static_cast<int64_t>(ints)}, c.dev);
+    int32_t* status = status_of(a[13], c.dev);
     if (ws.device() != c.dev || !ws.is_contiguous()) throw Refused("workspace must be contiguous and on " + c.dev.str());
     const c10::cuda::CUDAGuard guard(c.dev);
     at::Tensor out, lse;
@@ -313,12 +314,12 @@ PyObject* do_varlen(PyObject* const* a)
     if (scratch_bytes) scratch = at::empty({static_cast<int64_t>(scratch_bytes)}, c.t.options());
     int st = MLA_OK;
     if (batch != 0 && total_q != 0)
-        st = mla_decode_varlen(q.data_ptr(), static_cast<int>(total_q), static_cast<int>(h_q), c.d_qk, c.t.data_ptr(), c.num_blocks, c.page,
+        st = mla_decode_varlen_status(q.data_ptr(), static_cast<int>(total_q), static_cast<int>(h_q), c.d_qk, c.t.data_ptr(), c.num_blocks, c.page,
                                c.h_kv, table.data_ptr<int32_t>(), static_cast<int>(batch), as_int(table.size(1), "max_blocks"),
                                lens.data_ptr<int32_t>(), dv, c.dtype,
                                plan.data_ptr<int32_t>(), parts, static_cast<float>(float_arg(a[8], "softmax_scale")), out.data_ptr(),
                                lse.data_ptr<float>(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                               scratch_bytes ? scratch.data_ptr() : nullptr, scratch_bytes, stream_of(c.dev));
+                               scratch_bytes ? scratch.data_ptr() : nullptr, scratch_bytes, status, stream_of(c.dev));
     return Py_BuildValue("(iNN)", st, THPVariable_Wrap(out), THPVariable_Wrap(lse));
 }
 
@@ -353,7 +354,7 @@ PyMethodDef methods[] = {
     method<do_summarize, 8>("summarize"),
     method<do_select, 10>("select"),
     method<do_varlen_plan, 9>("varlen_plan"),
-    method<do_varlen, 13>("varlen"),
+    method<do_varlen, 14>("varlen"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -8,7 +8,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .api import flash_mla_with_kvcache, get_mla_metadata, workspace_bytes, workspace_zero_bytes
+from .api import DecodeCall, get_mla_metadata, workspace_bytes, workspace_zero_bytes
 
 
 def mla_select_pages(q: torch.Tensor, page_keys: torch.Tensor, page_scales: torch.Tensor, block_table: torch.Tensor,
@@ -41,7 +41,8 @@ def flash_mla_page_sparse(q: torch.Tensor, kvcache: torch.Tensor, block_table: t
 
     The selection of ``mla_select_pages`` (with the same arguments), then the paged decode over it; a
     token that sees at most ``topn`` pages attends all of them.  ``kvcache`` and ``is_fp8_kvcache`` as for
-    ``flash_mla_with_kvcache``; the lse is that of the attended rows.
+    ``flash_mla_with_kvcache``; the lse is that of the attended rows.  ``status`` int32 [1]: receives a
+    device-side error of the selection or the decode (without it, the decode's goes to the workspace).
     """
     table, lens = mla_select_pages(q, page_keys, page_scales, block_table, cache_seqlens, topn, n_first=n_first, n_last=n_last,
                                    causal=causal, status=status)
@@ -53,6 +54,6 @@ def flash_mla_page_sparse(q: torch.Tensor, kvcache: torch.Tensor, block_table: t
                 # the graph's own, zeroed by each replay: two graphs captured on one stream may be replayed on two
                 workspace = torch.empty(workspace_bytes(b * s_q, 1, h_q, 1, md.shape[0]), dtype=torch.uint8, device=q.device)
                 workspace[:workspace_zero_bytes(b * s_q, 1, h_q, 1)].zero_()
-    o, lse = flash_mla_with_kvcache(q.view(b * s_q, 1, h_q, d_qk), kvcache, table, lens, dv, md, num_splits, False,
-                                    is_fp8_kvcache, softmax_scale=softmax_scale, workspace=workspace)
+    o, lse = DecodeCall(q.view(b * s_q, 1, h_q, d_qk), kvcache, table, lens, dv, md, num_splits, is_fp8_kvcache=is_fp8_kvcache,
+                        softmax_scale=softmax_scale, workspace=workspace, status=status).run()
     return o.view(b, s_q, h_q, dv), lse.view(b, s_q, h_q)

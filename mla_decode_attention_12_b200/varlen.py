@@ -97,14 +97,16 @@ def flash_mla_varlen_with_kvcache(q: torch.Tensor, kvcache: torch.Tensor, block_
                                   cu_seqlens_q: torch.Tensor, cache_seqlens: torch.Tensor, dv: int, plan: VarlenPlan,
                                   causal: bool = True, is_fp8_kvcache: bool = False, *, softmax_scale: float | None = None,
                                   workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                                  lse: torch.Tensor | None = None):
+                                  lse: torch.Tensor | None = None, status: torch.Tensor | None = None):
     """MLA attention of ragged runs over a paged cache; ``(o [total_q, h_q, dv], lse [total_q, h_q] float32)``.
 
     ``q`` [total_q, h_q, d_qk]; ``kvcache``, ``block_table`` [batch, max_blocks] and the FP8 cache as for
     ``flash_mla_with_kvcache``.  Token i of a run of n tokens over L cached ones sees the first
     ``L - n + 1 + i`` of them (``causal``), or all L.  ``plan`` comes from ``get_mla_metadata_varlen``
     with the same ``cu_seqlens_q``, ``cache_seqlens`` and ``causal``.  Rows past ``cu_seqlens_q[batch]`` are
-    not written (of ``out`` and ``lse`` passed in, they stay as they were).
+    not written (of ``out`` and ``lse`` passed in, they stay as they were).  ``status`` int32 [1]: receives a
+    device-side error of the call (a block-table entry outside the cache, a length beyond the table, runs
+    that do not split the tokens); without it, the error goes to the workspace.
     """
     data, batch, total_q, h_q, num_parts, planned_causal = plan
     if q.dim() != 3 or (batch, total_q, h_q, planned_causal) != (cache_seqlens.numel(), q.shape[0], q.shape[1], bool(causal)):
@@ -113,7 +115,7 @@ def flash_mla_varlen_with_kvcache(q: torch.Tensor, kvcache: torch.Tensor, block_
         workspace = _call_workspace(num_parts, q.device)
     scale = 0.0 if softmax_scale is None else softmax_scale  # 0: 1 / sqrt(d_qk)
     st, out, lse = _lib.binding().varlen(q, kvcache, block_table, cu_seqlens_q, cache_seqlens, dv, data, num_parts, scale,
-                                         bool(is_fp8_kvcache), workspace, out, lse)
+                                         bool(is_fp8_kvcache), workspace, out, lse, status)
     if st:
         _lib.check(st, "mla_decode_varlen")
     return out, lse

@@ -183,3 +183,69 @@ def test_a_dense_wait_that_gave_up_leaves_the_counters_zero(withholding_lib):
     assert untouched(o[:1], lse[:1]).all() and not untouched(o, lse).all()
     check(s, *dense(s, workspace=ws))
     assert mla.read_device_status(ws) == 5
+
+
+@pytest.mark.parametrize("error", ["length", "page", "runs"])
+def test_status_of_a_ragged_call(error):
+    bad, only = with_error(error)
+    good = healthy()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(mla.varlen_workspace_bytes(mla.num_sm_parts()), dtype=torch.uint8, device="cuda")
+
+    def call(s):
+        d = on_gpu(s)
+        plan = mla.get_mla_metadata_varlen(d["cu"], d["seqlens"], 2, 64)
+        o, lse = sentinels(s)
+        return mla.flash_mla_varlen_with_kvcache(d["q"], d["cache"], d["table"], d["cu"], d["seqlens"], DV, plan,
+                                                 softmax_scale=s["scale"], workspace=ws, out=o, lse=lse, status=status)
+
+    check(bad, *call(bad), only=only)
+    assert int(status) == 6 and not ws[:mla.workspace_zero_bytes(1, 1, 1, 1)].any()
+    check(good, *call(good))
+    assert int(status) == 6  # the first error stays
+    status.zero_()
+    check(good, *call(good))
+    assert int(status) == 0
+
+
+def test_status_of_a_dequantized_page():
+    s = make("fp8", [5, 9], [140, 260], 128, seed=57)
+    d = on_gpu(s)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    plan = mla.get_mla_metadata_varlen(d["cu"], d["seqlens"], 14, 128, is_fp8_kvcache=True)
+    for table, want in ((d["table"].masked_fill(torch.arange(d["table"].shape[1]).cuda() == 1, -1), 6), (d["table"], 0)):
+        status.zero_()
+        o, lse = mla.flash_mla_varlen_with_kvcache(d["q"], d["cache"], table, d["cu"], d["seqlens"], DV, plan, True, True,
+                                                   softmax_scale=s["scale"], status=status)
+        assert int(status) == want
+    check(s, o, lse)
+
+
+def test_status_of_a_page_sparse_decode():
+    heads, lens = 16, [64 * 40, 64 * 30]
+    s = make("bf16", [1, 1], lens, heads, seed=58)
+    pages = s["cache"].shape[0]
+    keys, scales = torch.zeros(pages, 576, dtype=torch.int8).cuda(), torch.zeros(pages).cuda()
+    d = on_gpu(s)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call(table, topn):
+        status.zero_()
+        return mla.flash_mla_page_sparse(d["q"].view(2, 1, heads, 576), d["cache"], table, d["seqlens"], DV, keys, scales, topn,
+                                         status=status)
+
+    bad = d["table"].clone()
+    bad[0, 0] = pages
+    for topn in (8, 64):
+        call(bad, topn)
+        assert int(status) == 6
+        o, lse = call(d["table"], topn)
+        assert int(status) == 0
+    check(s, o.view(2, heads, DV), lse.view(2, heads))
+    for refused in (torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            mla.flash_mla_page_sparse(d["q"].view(2, 1, heads, 576), d["cache"], d["table"], d["seqlens"], DV, keys, scales, 8,
+                                      status=refused)
+        with pytest.raises(ValueError):
+            mla.flash_mla_varlen_with_kvcache(d["q"], d["cache"], d["table"], d["cu"], d["seqlens"], DV,
+                                              mla.get_mla_metadata_varlen(d["cu"], d["seqlens"], 2, heads), status=refused)
