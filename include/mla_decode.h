@@ -494,7 +494,7 @@ MLA_API mla_status mla_summarize_pages(const void* kvcache, int num_blocks, int 
  *                  512, h_q <= 128
  *   page_keys      device int8 [num_blocks, d_qk], 16-byte aligned;  page_scales device float32 [num_blocks]
  *   block_table    device int32 [batch, max_blocks_per_seq];  cache_seqlens device int32 [batch]
- *   topn >= n_first + n_last, n_first >= 0, n_last >= 1
+ *   topn >= n_first + n_last, n_first >= 0, n_last >= 1, topn < 2^25
  *   page_table     device int32 [batch * s_q, topn], written;  page_seqlens device int32 [batch * s_q], written
  *   workspace      device, >= mla_select_workspace_bytes(...), 16-byte aligned, any contents
  *   device_status  device int32 or null: records MLA_ERR_DEVICE_CHECK for a block-table entry outside

@@ -776,7 +776,10 @@ mla_status mla_select_pages(const void* q, int batch, int s_q, int h_q, int d_qk
     if (dtype != MLA_BF16 && dtype != MLA_FP16) return dtype == MLA_BF16_FP8KV ? MLA_ERR_UNSUPPORTED : MLA_ERR_INVALID_ARG;
     if (n_first < 0 || n_last < 1 || topn < 1 || n_first > topn || n_last > topn - n_first) return MLA_ERR_INVALID_ARG;
     if ((d_qk != 576 && d_qk != 512) || h_q > kMaxHeads) return MLA_ERR_UNSUPPORTED;
-    if (static_cast<long long>(num_blocks) * kPage >= (1ll << 31) || static_cast<long long>(max_blocks_per_seq) * kPage >= (1ll << 31))
+    // rows of a cache, and of a block table (topn columns of the chosen pages' one), are counted in int32
+    constexpr long long kMostRows = 1ll << 31;
+    if (static_cast<long long>(num_blocks) * kPage >= kMostRows || static_cast<long long>(max_blocks_per_seq) * kPage >= kMostRows ||
+        static_cast<long long>(topn) * kPage >= kMostRows)
         return MLA_ERR_UNSUPPORTED;
     const long long tokens = static_cast<long long>(batch) * s_q;
     // the line of tiles is counted in int32
