@@ -461,7 +461,7 @@ MLA_API mla_status mla_append_kvcache(const void* latent, long long latent_strid
  * they were.  A page with infinities or NaN gets an unspecified key.
  *
  *   kvcache, dtype, d_qk   as for mla_append_kvcache
- *   block_table    device int32 [batch, max_blocks_per_seq], fewer than 2^31 entries
+ *   block_table    device int32 [batch, max_blocks_per_seq], fewer than 2^31 entries; batch <= 2^30
  *   prev_seqlens, cache_seqlens   device int32 [batch]
  *   page_keys      device int8 [num_blocks, d_qk], 16-byte aligned;  page_scales float32 [num_blocks]
  *   device_status  device int32 or null: an entry outside the cache (skipped), or a length beyond the

@@ -613,7 +613,8 @@ mla_status mla_summarize_pages(const void* kvcache, int num_blocks, int page_siz
     if (page_size != kPage || h_kv != 1 || (d_qk != 576 && d_qk != 512) || (fp8 && d_qk != 576)) return MLA_ERR_UNSUPPORTED;
     if (static_cast<long long>(num_blocks) * kPage >= (1ll << 31)) return MLA_ERR_UNSUPPORTED;
     const long long most = static_cast<long long>(batch) * max_blocks_per_seq;  // pages that a step can complete: counted in int32
-    if (most >= (1ll << 31)) return MLA_ERR_UNSUPPORTED;
+    // (requests are counted in steps of a chunk)
+    if (most >= (1ll << 31) || batch > (1 << 30)) return MLA_ERR_UNSUPPORTED;
     if (batch == 0) return MLA_OK;
     if (!kvcache || !block_table || !prev_seqlens || !cache_seqlens || !page_keys || !page_scales) return MLA_ERR_INVALID_ARG;
     if (!aligned16(kvcache) || !aligned16(page_keys) || (reinterpret_cast<uintptr_t>(page_scales) & 3)) return MLA_ERR_INVALID_ARG;
