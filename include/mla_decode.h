@@ -453,8 +453,8 @@ MLA_API mla_status mla_append_kvcache(const void* latent, long long latent_strid
  * For every page j of request b with prev_seqlens[b] / 64 <= j < cache_seqlens[b] / 64 (whole
  * divisions: the pages that the tokens between the two lengths completed; a page that is not full
  * has no key), with rows r_0 .. r_63 at physical page P = block_table[b][j]:
- *   m              = (r_0 + ... + r_63) / 64          (right to the last bit of float32, whatever the
- *                                                      order: the sum is kept to about 48 bits)
+ *   m              = (r_0 + ... + r_63) / 64          (float32: rounded once from a sum within 2^-40 of
+ *                                                      sum |r_i| / 64; no order of finite rows overflows)
  *   page_scales[P] = max(max_i |m_i| * (1/127), 2^-126)                     (float32)
  *   page_keys[P]   = m_i / page_scales[P], rounded to float32 and then to the nearest whole number
  * An FP8 cache's latents are bf16(e4m3 * scale), as for attention.  Other pages' keys are left as

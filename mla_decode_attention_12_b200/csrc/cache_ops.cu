@@ -295,7 +295,7 @@ static_assert(kSumWorkers % 32 == 0 && 2 * kSumWorkers >= 576 && kSumRows >= 1, 
 static_assert(SumLayout<false>::kStageBytes % 128 == 0 && SumLayout<true>::kStageBytes % 128 == 0 &&
                   SumLayout<false>::kOffBar % 8 == 0 && SumLayout<true>::kOffBar % 8 == 0, "alignment");
 
-// Sums of pairs of columns that keep what each addition rounds away: hi + lo carries about 48 bits.
+// Sums of pairs of columns that keep what each addition rounds away (in 24 bits: the bound is below).
 struct Sum2 {
     float2 hi = {0.f, 0.f}, lo = {0.f, 0.f};
 
@@ -308,9 +308,13 @@ struct Sum2 {
 };
 
 // Key of a page: the mean of its 64 rows, as 8-bit whole numbers and a scale.  Bound by reading
-// the page (73.7 KB of 16-bit rows).  The key's rounding must not depend on the order of the sum,
-// so each sum is a pair of floats of about 48 bits together, kept by packed additions (two columns
-// an instruction, seven per pair of values).
+// the page (73.7 KB of 16-bit rows).  The key's rounding should not depend on the order of the sum,
+// so each sum is a pair of floats, kept by packed additions (two columns an instruction, seven per
+// pair of values, eight for bfloat16).  With u = 2^-24 and S = sum |r| / 64, what the pair loses: a thread's 16 additions
+// round their low parts by at most (1 + 2 + ... + 16) u u S, the 4 phases' meeting by (10 + 64 + 20) u u S:
+// less than 2^-40 S together, before the one rounding to float32.  bfloat16 rows are divided by 64 before they
+// are added (exact: 2^-139 is the least), so that no partial sum passes the largest float; float16 rows
+// cannot get there and are divided at the end.
 // Two blocks per SM take every gridDim-th of the list of completed pages, which all blocks derive
 // alike (prefix sums over requests).  A block's loader thread looks the pages up and keeps a ring of
 // half pages full by bulk copies (a page's rows are contiguous); thread (g, phase) adds columns
@@ -322,6 +326,13 @@ template <bool kFp16, bool kFp8>
 __global__ void __launch_bounds__(kSumThreads, 2) mla_summarize_kernel(const SummarizeParams p)
 {
     using L = SumLayout<kFp8>;
+    // two values of a row, as they are added
+    auto term = [](uint32_t w) {
+        if constexpr (kFp16)
+            return unpack16<true>(w);
+        else
+            return fmul2(unpack16<false>(w), make_float2(1.0f / kPage, 1.0f / kPage));
+    };
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     // partial sums of columns 8 g + 2 k, + 1: part[2 phase][k][g] and what they rounded away: part[2 phase + 1][k][g]
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) mla_summarize_kernel(const Sum
                                     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
                                         static_cast<__nv_fp8x2_storage_t>(w >> (16 * (k & 1))), __NV_E4M3);
                                     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                                    acc[k].add(unpack16<false>(pack16<false>(f.x * sc, f.y * sc)));
+                                    acc[k].add(term(pack16<false>(f.x * sc, f.y * sc)));
                                 }
                             }
                         } else {
@@ -447,7 +458,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) mla_summarize_kernel(const Sum
                                 const uint4 raw = *reinterpret_cast<const uint4*>(col + r * stride);
                                 const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) acc[k].add(unpack16<kFp16>(w[k]));
+                                for (int k = 0; k < 4; ++k) acc[k].add(term(w[k]));
                             }
                         }
                     }
@@ -472,8 +483,9 @@ __global__ void __launch_bounds__(kSumThreads, 2) mla_summarize_kernel(const Sum
                         rest = fadd2(rest, part[2 * q + 1][tid & 3][tid >> 2]);
                     }
                     rest = fadd2(rest, sum.lo);
-                    m0 = __fmul_rn(__fadd_rn(sum.hi.x, rest.x), 1.0f / kPage);
-                    m1 = __fmul_rn(__fadd_rn(sum.hi.y, rest.y), 1.0f / kPage);
+                    constexpr float kLeft = kFp16 ? 1.0f / kPage : 1.0f;  // (exact: no float16 mean is subnormal)
+                    m0 = __fmul_rn(__fadd_rn(sum.hi.x, rest.x), kLeft);
+                    m1 = __fmul_rn(__fadd_rn(sum.hi.y, rest.y), kLeft);
                 }
                 float mx = fmaxf(fabsf(m0), fabsf(m1));
 #pragma unroll
