@@ -1962,15 +1962,15 @@ __device__ __forceinline__ void dequantize16(const uint4 raw, const float s, uin
     hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// The pages of every run, dequantized once into scratch pages of 576 bfloat16 columns (page j of run b
-// is scratch page b * max_blocks + j) with their block table.  Memory bound: 1.8 KB per row.  One
+// The pages of every run with tokens, dequantized once into scratch pages of 576 bfloat16 columns (page j of
+// run b is scratch page b * max_blocks + j) with their block table; reads[b]: the rows of run b that its groups read.  Memory bound: 1.8 KB per row.  One
 // block per page: a warp takes 8 rows, lane l the latent columns [16 l, 16 l + 16) and position
 // columns 2 l, 2 l + 1 of each, four rows in flight.
 constexpr int kDequantThreads = 256;
 constexpr int kRow16 = 576 * 2;
 
 __global__ void __launch_bounds__(kDequantThreads) mla_dequantize_pages_kernel(const uint8_t* cache, const int32_t* block_table,
-                                                                               const int32_t* seqlens, int batch, int max_blocks,
+                                                                               const int32_t* reads, int batch, int max_blocks,
                                                                                int num_blocks, uint8_t* out, int32_t* out_table,
                                                                                int* status)
 {
@@ -1980,7 +1980,7 @@ __global__ void __launch_bounds__(kDequantThreads) mla_dequantize_pages_kernel(c
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
         const int b = static_cast<int>(u / max_blocks), j = static_cast<int>(u - static_cast<long long>(b) * max_blocks);
         if (threadIdx.x == 0) out_table[u] = static_cast<int>(u);
-        if (j >= pages_of(seqlens[b])) continue;
+        if (j >= pages_of(reads[b])) continue;
         int page = block_table[u];
         if (page < 0 || page >= num_blocks) {
             if (threadIdx.x == 0) atomicCAS(status, 0, MLA_ERR_DEVICE_CHECK);
@@ -2116,14 +2116,16 @@ static size_t metadata_smem_bytes(int nv, int num_parts)
 // per step, for every layer; starts and lengths are read once, into shared memory (up to 4,096 runs).  C: the prefix sums, in shared memory where they fit (a partition's
 // binary searches then take about 0.1 us instead of several), else behind the table.
 // Runs that are not an ascending split of the tokens give an empty schedule whose md rows carry an
-// error (field 5), which the decode records.
+// error (field 5), which the decode records.  Behind the table and the prefix sums: the rows that each run's groups
+// read (none for a run without tokens, whose length and pages may be stale).
 constexpr int kVarMaxRuns = 16384, kVarCachedRuns = 4096;
 
 template <int kVarThreads>
 __global__ void __launch_bounds__(kVarThreads) mla_metadata_varlen_kernel(const int32_t* cu, const int32_t* seqlens,
                                                                           int batch, int total_q, int h_q, int causal,
                                                                           int num_parts, int fixed_cost, int32_t* md,
-                                                                          int32_t* groups, long long* c_global)
+                                                                          int32_t* groups, long long* c_global,
+                                                                          int32_t* reads)
 {
     extern __shared__ __align__(16) uint8_t meta_smem[];
     grid_launch_dependents();
@@ -2154,6 +2156,7 @@ __global__ void __launch_bounds__(kVarThreads) mla_metadata_varlen_kernel(const 
     }
     __syncthreads();
     const bool skip = bad != 0;
+    for (int b = tid; b < batch; b += kVarThreads) reads[b] = skip ? 0 : run_reads(cu_s[b], cu_s[b + 1], len_s[b]);
     int nv = 0;
     block_exclusive_scan(first, batch, warp_tot_i, nv);
     if (skip) nv = 0;
@@ -2455,6 +2458,12 @@ static long long varlen_groups(int batch, int total_q, int h_q)
     return static_cast<long long>(total_q) * h_q / kRowsPerGroup + batch;
 }
 
+// Where the plan holds the rows that each run reads.
+static size_t varlen_reads_at(int batch, int total_q, int h_q, int num_parts)
+{
+    return static_cast<size_t>(num_parts) * kMdInts + static_cast<size_t>(varlen_groups(batch, total_q, h_q)) * (kVarInts + 2);
+}
+
 static mla_status check_varlen(int batch, int total_q, int h_q, int h_kv, int num_parts)
 {
     if (batch < 0 || total_q < 0 || h_q <= 0 || h_kv <= 0 || num_parts <= 0) return MLA_ERR_INVALID_ARG;
@@ -2490,8 +2499,8 @@ static size_t varlen_scratch_bytes(int batch, int total_q, int h_q, int max_bloc
 size_t mla_varlen_plan_ints(int batch, int total_q, int h_q, int h_kv, int num_parts)
 {
     if (check_varlen(batch, total_q, h_q, h_kv, num_parts) != MLA_OK) return 0;
-    // md rows, group table, cost prefixes (64 bits each)
-    return static_cast<size_t>(num_parts) * kMdInts + static_cast<size_t>(varlen_groups(batch, total_q, h_q)) * (kVarInts + 2);
+    // md rows, group table, cost prefixes (64 bits each), rows that each run reads
+    return varlen_reads_at(batch, total_q, h_q, num_parts) + static_cast<size_t>(batch);
 }
 
 mla_status mla_get_metadata_varlen(const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, int batch, int total_q,
@@ -2527,7 +2536,7 @@ mla_status mla_get_metadata_varlen(const int32_t* cu_seqlens_q, const int32_t* c
     }
     kern<<<1, few ? 256 : 1024, smem, static_cast<cudaStream_t>(stream)>>>(
         cu_seqlens_q, cache_seqlens, batch, total_q, h_q, causal, num_parts, varlen_fixed_cost(is_fp8_kvcache, batch, total_q, h_q),
-        plan, groups, c_global);
+        plan, groups, c_global, plan + varlen_reads_at(batch, total_q, h_q, num_parts));
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -2544,7 +2553,8 @@ mla_status mla_get_metadata_varlen_host(const int32_t* cu_seqlens_q, const int32
                          varlen_fixed_cost(is_fp8_kvcache, batch, total_q, h_q), plan,
                          plan + static_cast<size_t>(num_parts) * kMdInts,
                          reinterpret_cast<long long*>(plan + static_cast<size_t>(num_parts) * kMdInts +
-                                                      static_cast<size_t>(varlen_groups(batch, total_q, h_q)) * kVarInts));
+                                                      static_cast<size_t>(varlen_groups(batch, total_q, h_q)) * kVarInts),
+                         plan + varlen_reads_at(batch, total_q, h_q, num_parts));
     return MLA_OK;
 }
 
@@ -2954,7 +2964,8 @@ mla_status mla_decode_varlen_status(const void* q, int total_q, int h_q, int d_q
         if (!sm_count(&sms)) return MLA_ERR_CUDA;
         const int blocks = pages < 8ll * sms ? static_cast<int>(pages) : 8 * sms;
         mla_dequantize_pages_kernel<<<blocks, kDequantThreads, 0, st>>>(static_cast<const uint8_t*>(kvcache), block_table,
-                                                                       cache_seqlens, batch, max_blocks_per_seq, num_blocks,
+                                                                       plan + varlen_reads_at(batch, total_q, h_q, num_parts),
+                                                                       batch, max_blocks_per_seq, num_blocks,
                                                                        pages16, table16, prm.status);
         if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
         fp8 = false;

@@ -100,10 +100,18 @@ MLA_HD inline int clamp_seen(long long seen, int len)
     return seen < 0 ? 0 : (seen < len ? static_cast<int>(seen) : len);
 }
 
+constexpr int kVarMostRows = 1 << 30;  // no cache holds as many rows; page counts stay in 32 bits
+
+// Cached rows that the groups of a run of tokens [t0, t1) read (its last token sees them all).
+MLA_HD inline int run_reads(int t0, int t1, int len)
+{
+    return t1 <= t0 || len < 0 ? 0 : (len < kVarMostRows ? len : kVarMostRows);
+}
+
 // Group g of run b = tokens [t0, t1): its row of the table (kVarSplits = 1).
 MLA_HD inline void fill_group(int32_t* gr, int b, int g, int t0, int t1, int len, int h_q, bool causal)
 {
-    if (len > (1 << 30)) len = 1 << 30;  // no cache holds as many rows; page counts stay in 32 bits
+    if (len > kVarMostRows) len = kVarMostRows;
     const int row0 = t0 * h_q + g * kRowsPerGroup, end = t1 * h_q;
     const int rows = end - row0 < kRowsPerGroup ? end - row0 : kRowsPerGroup;
     const int seen = run_seen(t1, len, causal);
@@ -210,11 +218,12 @@ inline void schedule_host(const int32_t* seqlens, int batch, int groups, int num
     num_splits[nv] = acc;
 }
 
-// The same for ragged runs: group table and md rows.  Scratch: C [groups].
+// The same for ragged runs: group table, md rows and the rows that each run reads.  Scratch: C [groups].
 inline void schedule_varlen_host(const int32_t* cu, const int32_t* seqlens, int batch, int h_q, bool causal, int num_parts,
-                                 int F, int32_t* md, int32_t* groups, long long* C)
+                                 int F, int32_t* md, int32_t* groups, long long* C, int32_t* reads)
 {
     int nv = 0;
+    for (int b = 0; b < batch; ++b) reads[b] = run_reads(cu[b], cu[b + 1], seqlens[b]);
     for (int b = 0; b < batch; ++b) nv += row_groups((cu[b + 1] - cu[b]) * h_q);
     // C, until it holds the prefix sums: the place of each group on the line
     for (int i = 0; i < nv; ++i) C[group_on_line(i, nv, num_parts)] = i;
