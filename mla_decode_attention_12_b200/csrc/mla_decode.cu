@@ -2343,14 +2343,12 @@ static mla_status launch_metadata(const int32_t* seqlens, int const_len, int bat
     const int nv = batch * row_groups(heads_per_kv);
     const size_t smem = metadata_smem_bytes(nv, num_parts);
     if (smem > 200 * 1024) return MLA_ERR_UNSUPPORTED;  // the schedule is built in one CTA's shared memory
-    if (smem > 48 * 1024) {
-        static PerDeviceOnce configured;
-        if (configured.run([] {
-                return cudaFuncSetAttribute(mla_metadata_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            200 * 1024);
-            }) != cudaSuccess)
-            return MLA_ERR_CUDA;
-    }
+    // (whatever the size: the 48 KB that need no set-up hold the kernel's static shared memory too)
+    static PerDeviceOnce configured;
+    if (configured.run([] {
+            return cudaFuncSetAttribute(mla_metadata_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+        }) != cudaSuccess)
+        return MLA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     programmatic_launch(cfg, attr, dim3(1), dim3(kMetaThreads), smem, static_cast<cudaStream_t>(stream));
@@ -2524,16 +2522,14 @@ mla_status mla_get_metadata_varlen(const int32_t* cu_seqlens_q, const int32_t* c
     }
     const bool few = most <= 512 && batch <= 512;
     auto kern = few ? mla_metadata_varlen_kernel<256> : mla_metadata_varlen_kernel<1024>;
-    if (smem > 48 * 1024) {
-        static PerDeviceOnce configured;
-        if (configured.run([] {
-                const cudaError_t e = cudaFuncSetAttribute(mla_metadata_varlen_kernel<256>,
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-                return e != cudaSuccess ? e : cudaFuncSetAttribute(mla_metadata_varlen_kernel<1024>,
-                                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-            }) != cudaSuccess)
-            return MLA_ERR_CUDA;
-    }
+    static PerDeviceOnce configured;  // (whatever the size, as for the dense schedule)
+    if (configured.run([] {
+            const cudaError_t e = cudaFuncSetAttribute(mla_metadata_varlen_kernel<256>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+            return e != cudaSuccess ? e : cudaFuncSetAttribute(mla_metadata_varlen_kernel<1024>,
+                                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        }) != cudaSuccess)
+        return MLA_ERR_CUDA;
     kern<<<1, few ? 256 : 1024, smem, static_cast<cudaStream_t>(stream)>>>(
         cu_seqlens_q, cache_seqlens, batch, total_q, h_q, causal, num_parts, varlen_fixed_cost(is_fp8_kvcache, batch, total_q, h_q),
         plan, groups, c_global, plan + varlen_reads_at(batch, total_q, h_q, num_parts));
