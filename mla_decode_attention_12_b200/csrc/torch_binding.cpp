@@ -89,15 +89,17 @@ int as_int(int64_t v, const char* name)
     return static_cast<int>(v);
 }
 
-int int_arg(PyObject* o, const char* name)
+int64_t int64_arg(PyObject* o, const char* name)
 {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) {
         PyErr_Clear();
         throw Refused(std::string(name) + " must be an integer");
     }
-    return as_int(v, name);
+    return v;
 }
+
+int int_arg(PyObject* o, const char* name) { return as_int(int64_arg(o, name), name); }
 
 double float_arg(PyObject* o, const char* name)
 {
@@ -272,7 +274,8 @@ PyObject* do_varlen_plan(PyObject* const* a)
     return Py_BuildValue("(iiN)", st, parts, THPVariable_Wrap(plan));
 }
 
-// varlen(q, kvcache, block_table, cu_seqlens_q, cache_seqlens, dv, plan, num_parts, softmax_scale, fp8, workspace, out, lse, status)
+// varlen(q, kvcache, block_table, cu_seqlens_q, cache_seqlens, dv, plan, num_parts, softmax_scale, fp8, workspace, out, lse, status,
+//        max_scratch_bytes)
 //   -> (status, out, lse)
 PyObject* do_varlen(PyObject* const* a)
 {
@@ -306,12 +309,24 @@ PyObject* do_varlen(PyObject* const* a)
     } else {
         lse = at::empty({total_q, h_q}, q.options().dtype(at::kFloat));
     }
-    // FP8 pages that several groups read are dequantized once, into memory of this call alone
-    const size_t scratch_bytes = c.dtype != MLA_BF16_FP8KV ? 0
+    // FP8 pages that several groups read are dequantized once, into memory of this call alone, or, where the
+    // caller or the device has not that much to give, at every read
+    size_t scratch_bytes = c.dtype != MLA_BF16_FP8KV ? 0
         : mla_decode_varlen_scratch_bytes(static_cast<int>(batch), static_cast<int>(total_q), static_cast<int>(h_q),
                                           as_int(table.size(1), "max_blocks"), c.dtype);
+    if (a[14] != Py_None) {
+        const int64_t most = int64_arg(a[14], "max_scratch_bytes");
+        if (most < 0) throw Refused("max_scratch_bytes must not be negative");
+        if (scratch_bytes > static_cast<size_t>(most)) scratch_bytes = 0;
+    }
     at::Tensor scratch;
-    if (scratch_bytes) scratch = at::empty({static_cast<int64_t>(scratch_bytes)}, c.t.options());
+    if (scratch_bytes) {
+        try {
+            scratch = at::empty({static_cast<int64_t>(scratch_bytes)}, c.t.options());
+        } catch (const c10::OutOfMemoryError&) {
+            scratch_bytes = 0;
+        }
+    }
     int st = MLA_OK;
     if (batch != 0 && total_q != 0)
         st = mla_decode_varlen_status(q.data_ptr(), static_cast<int>(total_q), static_cast<int>(h_q), c.d_qk, c.t.data_ptr(), c.num_blocks, c.page,
@@ -354,7 +369,7 @@ PyMethodDef methods[] = {
     method<do_summarize, 8>("summarize"),
     method<do_select, 10>("select"),
     method<do_varlen_plan, 9>("varlen_plan"),
-    method<do_varlen, 14>("varlen"),
+    method<do_varlen, 15>("varlen"),
     {nullptr, nullptr, 0, nullptr},
 };
 

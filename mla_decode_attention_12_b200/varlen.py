@@ -97,7 +97,8 @@ def flash_mla_varlen_with_kvcache(q: torch.Tensor, kvcache: torch.Tensor, block_
                                   cu_seqlens_q: torch.Tensor, cache_seqlens: torch.Tensor, dv: int, plan: VarlenPlan,
                                   causal: bool = True, is_fp8_kvcache: bool = False, *, softmax_scale: float | None = None,
                                   workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                                  lse: torch.Tensor | None = None, status: torch.Tensor | None = None):
+                                  lse: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                                  max_scratch_bytes: int | None = None):
     """MLA attention of ragged runs over a paged cache; ``(o [total_q, h_q, dv], lse [total_q, h_q] float32)``.
 
     ``q`` [total_q, h_q, d_qk]; ``kvcache``, ``block_table`` [batch, max_blocks] and the FP8 cache as for
@@ -107,6 +108,12 @@ def flash_mla_varlen_with_kvcache(q: torch.Tensor, kvcache: torch.Tensor, block_
     not written (of ``out`` and ``lse`` passed in, they stay as they were).  ``status`` int32 [1]: receives a
     device-side error of the call (a block-table entry outside the cache, a length beyond the table, runs
     that do not split the tokens); without it, the error goes to the workspace.
+
+    Over an FP8 cache, runs of about three groups of 128 query rows and more have their pages dequantized
+    once, into 73.7 KB for every entry of the block table (whatever the lengths), allocated for the call: up to
+    ``max_scratch_bytes`` (8 GiB, if None).  A call that would need more, or does not get it, reads the FP8 rows
+    at every use: slower, with no memory of its own.  Where the memory is known to be missing,
+    ``max_scratch_bytes=0`` spares each call the attempt.
     """
     data, batch, total_q, h_q, num_parts, planned_causal = plan
     if q.dim() != 3 or (batch, total_q, h_q, planned_causal) != (cache_seqlens.numel(), q.shape[0], q.shape[1], bool(causal)):
@@ -115,7 +122,7 @@ def flash_mla_varlen_with_kvcache(q: torch.Tensor, kvcache: torch.Tensor, block_
         workspace = _call_workspace(num_parts, q.device)
     scale = 0.0 if softmax_scale is None else softmax_scale  # 0: 1 / sqrt(d_qk)
     st, out, lse = _lib.binding().varlen(q, kvcache, block_table, cu_seqlens_q, cache_seqlens, dv, data, num_parts, scale,
-                                         bool(is_fp8_kvcache), workspace, out, lse, status)
+                                         bool(is_fp8_kvcache), workspace, out, lse, status, max_scratch_bytes)
     if st:
         _lib.check(st, "mla_decode_varlen")
     return out, lse
