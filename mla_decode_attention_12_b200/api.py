@@ -28,8 +28,15 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _with_index(device: torch.device) -> torch.device:
+    """A CUDA device by its index (the current one where it names none)."""
+    if device.type != "cuda":
+        raise ValueError(f"expected a CUDA device, got {device}")
+    return device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
 def _stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
+    return torch._C._cuda_getCurrentRawStream(_with_index(device).index)
 
 
 def num_sm_parts(device=None) -> int:
