@@ -154,11 +154,22 @@ def workspace_zero_bytes(batch: int, s_q: int, h_q: int, h_kv: int) -> int:
 def get_workspace(nbytes: int, device: torch.device, zero_bytes: int) -> torch.Tensor:
     """A cached, grow-only workspace per (device, stream) whose control block is zero.
 
+    Inside a graph capture, one of the graph's own instead, whose control block each replay zeroes: two
+    graphs captured on one stream may be replayed on two.
+
     ``zero_bytes`` is the control block's size (the same for every problem): it is
     zeroed when the workspace is allocated, and every call leaves its counters zero for the
     next call of any size.  Its status word keeps the first device error until
     ``read_device_status(ws, clear=True)``; calls go on working meanwhile.
     """
+    device = _with_index(device)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return get_workspace(nbytes, device, zero_bytes)
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(max(nbytes, zero_bytes), dtype=torch.uint8, device=device)
+        ws[:zero_bytes].zero_()
+        return ws
     key = (device.index, _stream(device))
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < max(nbytes, zero_bytes):

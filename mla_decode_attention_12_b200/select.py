@@ -8,7 +8,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .api import DecodeCall, get_mla_metadata, workspace_bytes, workspace_zero_bytes
+from .api import DecodeCall, get_mla_metadata
 
 
 def mla_select_pages(q: torch.Tensor, page_keys: torch.Tensor, page_scales: torch.Tensor, block_table: torch.Tensor,
@@ -48,12 +48,6 @@ def flash_mla_page_sparse(q: torch.Tensor, kvcache: torch.Tensor, block_table: t
                                    causal=causal, status=status)
     b, s_q, h_q, d_qk = q.shape
     md, num_splits = get_mla_metadata(lens, h_q, 1, is_fp8_kvcache=is_fp8_kvcache)
-    if workspace is None:
-        with torch.cuda.device(q.device):
-            if torch.cuda.is_current_stream_capturing():
-                # the graph's own, zeroed by each replay: two graphs captured on one stream may be replayed on two
-                workspace = torch.empty(workspace_bytes(b * s_q, 1, h_q, 1, md.shape[0]), dtype=torch.uint8, device=q.device)
-                workspace[:workspace_zero_bytes(b * s_q, 1, h_q, 1)].zero_()
     o, lse = DecodeCall(q.view(b * s_q, 1, h_q, d_qk), kvcache, table, lens, dv, md, num_splits, is_fp8_kvcache=is_fp8_kvcache,
                         softmax_scale=softmax_scale, workspace=workspace, status=status).run()
     return o.view(b, s_q, h_q, dv), lse.view(b, s_q, h_q)

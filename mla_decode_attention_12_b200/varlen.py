@@ -76,21 +76,13 @@ _varlen_bytes: dict = {}  # workspace size by partition count
 
 
 def _call_workspace(num_parts: int, dev: torch.device) -> torch.Tensor:
-    """The stream's cached workspace; inside a graph capture one of the graph's own, whose control block each replay
-    zeroes (two graphs captured on one stream may be replayed on two)."""
+    """The stream's cached workspace; inside a graph capture one of the graph's own."""
     if dev.type != "cuda":
         raise ValueError("q must be on a CUDA device")
     sizes = _varlen_bytes.get(num_parts)
     if sizes is None:
         sizes = _varlen_bytes[num_parts] = (varlen_workspace_bytes(num_parts), workspace_zero_bytes(1, 1, 1, 1))
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _call_workspace(num_parts, dev)
-    if not torch.cuda.is_current_stream_capturing():
-        return get_workspace(sizes[0], dev, sizes[1])
-    ws = torch.empty(sizes[0], dtype=torch.uint8, device=dev)
-    ws[:sizes[1]].zero_()
-    return ws
+    return get_workspace(sizes[0], dev, sizes[1])
 
 
 def flash_mla_varlen_with_kvcache(q: torch.Tensor, kvcache: torch.Tensor, block_table: torch.Tensor,
