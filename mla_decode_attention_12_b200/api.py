@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 
 import torch
 
@@ -21,7 +22,17 @@ from . import _lib
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 MLA_BF16_FP8KV = 2   # bfloat16 q / o over an "FP8 with scale" cache (656-byte rows)
 FP8_ROW_BYTES = 656
-_workspaces: dict = {}
+
+
+class _Workspaces(threading.local):
+    """Default workspaces of a host thread, by (device, stream): a call enqueues two kernels that share one, and calls
+    of two threads on one stream may interleave them."""
+
+    def __init__(self):
+        self.by_stream: dict = {}
+
+
+_workspaces = _Workspaces()
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -152,7 +163,7 @@ def workspace_zero_bytes(batch: int, s_q: int, h_q: int, h_kv: int) -> int:
 
 
 def get_workspace(nbytes: int, device: torch.device, zero_bytes: int) -> torch.Tensor:
-    """A cached, grow-only workspace per (device, stream) whose control block is zero.
+    """A cached, grow-only workspace per (device, stream, host thread) whose control block is zero.
 
     Inside a graph capture, one of the graph's own instead, whose control block each replay zeroes: two
     graphs captured on one stream may be replayed on two.
@@ -171,11 +182,11 @@ def get_workspace(nbytes: int, device: torch.device, zero_bytes: int) -> torch.T
         ws[:zero_bytes].zero_()
         return ws
     key = (device.index, _stream(device))
-    ws = _workspaces.get(key)
+    ws = _workspaces.by_stream.get(key)
     if ws is None or ws.numel() < max(nbytes, zero_bytes):
         ws = torch.empty(max(nbytes, zero_bytes), dtype=torch.uint8, device=device)
         ws[:zero_bytes].zero_()
-        _workspaces[key] = ws
+        _workspaces.by_stream[key] = ws
     return ws
 
 
