@@ -47,7 +47,8 @@ def _with_index(device: torch.device) -> torch.device:
 
 
 def _stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(_with_index(device).index)
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(_with_index(device).index if index is None else index)
 
 
 def num_sm_parts(device=None) -> int:
@@ -173,15 +174,18 @@ def get_workspace(nbytes: int, device: torch.device, zero_bytes: int) -> torch.T
     next call of any size.  Its status word keeps the first device error until
     ``read_device_status(ws, clear=True)``; calls go on working meanwhile.
     """
-    device = _with_index(device)
-    if device.index != torch.cuda.current_device():
+    # (once per layer: the C functions behind torch.cuda.current_device and the like take half a microsecond less)
+    if device.index is None or device.type != "cuda":
+        device = _with_index(device)
+    index = device.index
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return get_workspace(nbytes, device, zero_bytes)
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         ws = torch.empty(max(nbytes, zero_bytes), dtype=torch.uint8, device=device)
         ws[:zero_bytes].zero_()
         return ws
-    key = (device.index, _stream(device))
+    key = (index, torch._C._cuda_getCurrentRawStream(index))
     ws = _workspaces.by_stream.get(key)
     if ws is None or ws.numel() < max(nbytes, zero_bytes):
         ws = torch.empty(max(nbytes, zero_bytes), dtype=torch.uint8, device=device)
