@@ -105,7 +105,6 @@ constexpr int kQPrefetchPages = 8;         // pages before a chunk's end at whic
 #endif
 constexpr unsigned long long kWaitTimeoutNs = MLA_WAIT_TIMEOUT_NS;
 constexpr int kWorkspaceHeader = 256;
-constexpr int kSplitLost = 1 << 30;  // in the second counter of a virtual batch: one of its splits never came
 // The workspace's control block has room for the counters of this many virtual batches
 // (requests x row groups of 128 query rows), whatever the call: its size does not depend on
 // the problem, so the split partials of one call never overlap the counters of another.
@@ -1702,31 +1701,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             lo = nlo;
             hi = nhi;
         }
-        announce();
-        // A warp whose wait gave up in chunk vb announces the splits it leaves all the same, marked as
-        // lost: every call's counters reach their full counts, so that the combine can clear them
-        // and no later call finds them half counted.
-        if (!ok && lane == 0) {
-            ChunkIter<kVarlen> rest{md[0], md[1], md[2], md[3], p.batch, kVarlen ? p.vgroups : p.seqlens,
-                                    kVarlen ? p.max_blocks : p.topk};
-            int left, left_lo, left_hi;
-            while (rest.next(left, left_lo, left_hi)) {
-                if (left < vb) continue;
-                const int idx = (left == begin_vb) ? begin_split : 0;
-                int at = left;
-                bool split;
-                if constexpr (kVarlen) {
-                    split = p.vgroups[kVarInts * left + kVarSplits] > 1;
-                    at = idx > 0 ? part - idx + 1 : part + 1;
-                } else {
-                    split = p.num_splits[left + 1] - p.num_splits[left] > 1;
-                }
-                if (!split) continue;
-                atomicOr(p.ctl + 2 * at + 1, kSplitLost);
-                __threadfence();
-                atomicAdd(p.ctl + 2 * at, 1);
-            }
-        }
+        if (ok) announce();
         if (t == 0) TL_EV(kEvExit);
     }
 
@@ -1758,8 +1733,7 @@ __device__ __forceinline__ void combine_rows(const DecodeParams& p)
     // the wait below cannot starve its producers; it is bounded all the same.  The last
     // combine CTA of the virtual batch past the wait clears both counters for the next call.
     // (The schedule was written by the metadata grid, complete before the split-KV grid
-    // allowed this one to launch.)  A split that a cluster gave up is announced too, marked as lost:
-    // its virtual batch is not written, and its counters are cleared like the others.
+    // allowed this one to launch.)
     // blockIdx.x: the virtual batch, or, for ragged runs, the partition that holds its split 1 (at
     // most one split virtual batch starts its second split in a partition).
     int vb = blockIdx.x, slot0, nsplit, rows_here, row0 = 0;
@@ -1790,9 +1764,8 @@ __device__ __forceinline__ void combine_rows(const DecodeParams& p)
             __nanosleep(200);
             ready = ld_acquire_gpu(split_done) >= want;
             // Where a wait gave up (this one, or one that the status word tells of, from this call or an
-            // earlier one), the end of the split-KV grid decides: its own waits are bounded, and each of its
-            // clusters announces all its splits, lost ones too, so that only a combine without its split-KV
-            // pass finds too few.  Other recorded errors (a block-table entry outside the cache, a length
+            // earlier one), the end of the split-KV grid decides: its own waits are bounded, and no split is
+            // announced after it.  Other recorded errors (a block-table entry outside the cache, a length
             // beyond the table) lose no split.
             if (!ready && (global_timer_ns() - t0 > kWaitTimeoutNs || ld_acquire_gpu(p.status) == MLA_ERR_TIMEOUT)) {
                 grid_dependency_wait();
@@ -1801,15 +1774,12 @@ __device__ __forceinline__ void combine_rows(const DecodeParams& p)
                 break;
             }
         }
-        go = 0;
-        if (ready) {
-            const int passed = atomicAdd(combine_passed, 1);
-            if ((passed & ~kSplitLost) == static_cast<int>(gridDim.y) - 1) {
-                *combine_passed = 0;
-                *split_done = 0;
-            }
-            go = (passed & kSplitLost) == 0;  // rows that lost a split are not written
+        // (a virtual batch that lost a split is not written; its counters are cleared all the same)
+        if (atomicAdd(combine_passed, 1) == static_cast<int>(gridDim.y) - 1) {
+            *combine_passed = 0;
+            *split_done = 0;
         }
+        go = ready;
     }
     __syncthreads();
     if (!go) return;
@@ -1963,8 +1933,8 @@ __device__ __forceinline__ void dequantize16(const uint4 raw, const float s, uin
 }
 
 // The pages of every run with tokens, dequantized once into scratch pages of 576 bfloat16 columns (page j of
-// run b is scratch page b * max_blocks + j) with their block table; reads[b]: the rows of run b that its groups read.  Memory bound: 1.8 KB per row.  One
-// block per page: a warp takes 8 rows, lane l the latent columns [16 l, 16 l + 16) and position
+// run b is scratch page b * max_blocks + j) with their block table; reads[b]: the rows of run b that its
+// groups read.  Memory bound: 1.8 KB per row.  One block per page: a warp takes 8 rows, lane l the latent columns [16 l, 16 l + 16) and position
 // columns 2 l, 2 l + 1 of each, four rows in flight.
 constexpr int kDequantThreads = 256;
 constexpr int kRow16 = 576 * 2;
@@ -2143,9 +2113,8 @@ __global__ void __launch_bounds__(kVarThreads) mla_metadata_varlen_kernel(const 
     if (tid == 0) bad = 0;
     __syncthreads();
     for (int b = tid; b < batch; b += kVarThreads) {
-        const int t0 = cu[b], t1 = cu[b + 1];
+        const int t0 = cu[b], t1 = cu[b + 1], len = seqlens[b];
         if (small) {
-            const int len = seqlens[b];
             cached[b] = t0;
             if (b == batch - 1) cached[batch] = t1;
             cached[((batch + 2) & ~1) + b] = len;
@@ -2153,10 +2122,10 @@ __global__ void __launch_bounds__(kVarThreads) mla_metadata_varlen_kernel(const 
         const bool fine = t0 >= 0 && t1 >= t0 && t1 <= total_q;
         if (!fine) bad = 1;
         first[b] = fine ? row_groups((t1 - t0) * h_q) : 0;
+        reads[b] = fine ? run_reads(t0, t1, len) : 0;  // (an empty schedule's are read into scratch alone)
     }
     __syncthreads();
     const bool skip = bad != 0;
-    for (int b = tid; b < batch; b += kVarThreads) reads[b] = skip ? 0 : run_reads(cu_s[b], cu_s[b + 1], len_s[b]);
     int nv = 0;
     block_exclusive_scan(first, batch, warp_tot_i, nv);
     if (skip) nv = 0;

@@ -134,8 +134,8 @@ def untouched(o, lse):
 
 @pytest.mark.parametrize("parts", [4, 9])
 def test_a_wait_that_gave_up_leaves_the_counters_zero(withholding_lib, parts):
-    """Ragged runs: the aborted cluster announces the splits it leaves as lost; nothing of theirs is written, the others
-    are right, and the workspace serves the next call without being cleared."""
+    """Ragged runs: nothing of the aborted cluster's groups is written, the others are right, and the workspace serves the
+    next call without being cleared."""
     s = make("bf16", [1, 2, 1, 1], [3000, 5000, 700, 64], 128, seed=55)
     d = on_gpu(s)
     plan = mla.get_mla_metadata_varlen(d["cu"], d["seqlens"], 5, 128, num_parts=parts)
