@@ -349,7 +349,8 @@ MLA_API mla_status mla_sparse_prefill(const void* q, int s_q, int h_q, int d_qk,
  *   x_j  = softmax_scale * <q[t,h,:], k_j>  (j < n),  lse = log(sum_j exp(x_j))   (-inf when n = 0)
  *   o    = sum_j exp(x_j - lse) * k_j[0:512]                                       (0 when n = 0)
  * Cached rows past the last one that a group of 128 query rows (tokens x heads) sees are not read into its
- * result, whatever they hold.  Rows of q, o and lse past cu_seqlens_q[batch] are left as they were.
+ * result, whatever they hold; rows that only some of the group's tokens see have weight zero for the others,
+ * so that infinities or NaN in them reach the whole group.  Rows of q, o and lse past cu_seqlens_q[batch] are left as they were.
  *
  * mla_get_metadata_varlen: the tile scheduler, once per step for every layer.  Each run's rows are cut
  *   into groups of 128; a group's work is the pages that its last token sees.
@@ -372,7 +373,8 @@ MLA_API mla_status mla_sparse_prefill(const void* q, int s_q, int h_q, int d_qk,
  *                  null.  Over an FP8 cache, runs of several groups read each page several times: with
  *                  scratch their pages are dequantized once into it (the same values); without, at
  *                  every read.  mla_decode_varlen_scratch_bytes is 0 where it would not pay (16-bit
- *                  caches, fewer than three groups per run) or would exceed 8 GiB.
+ *                  caches, fewer than three groups per run on average) or would exceed 8 GiB.  (The
+ *                  schedule balances for the dequantized pages then; it is valid without scratch too.)
  *   Enqueues the split-KV and the combine kernel on `stream` (and, with scratch, one before them).
  * mla_decode_varlen_status: the same, with the call's device errors recorded in *device_status (device int32; the
  *   first error if it holds 0) instead of the workspace's status word; null: as mla_decode_varlen.

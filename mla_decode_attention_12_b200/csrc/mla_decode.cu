@@ -26,11 +26,15 @@
 //   t / 64), a K loader, the MMA issuer, a V loader (zeroes page tails), a Q loader.
 //   Pages are gathered through the block table by TMA.
 // * Online softmax in base 2 with a lazily moved reference maximum: O is rescaled in
-//   tensor memory only when the running maximum grows by more than 2^8.
-// * Epilogue: the softmax warps store the next chunk's Q into tensor memory, then drain
-//   O 64 columns at a time into swizzled tiles handed to TMA bulk stores: 16-bit O for
-//   unsplit chunks, fp32 partials and LSEs for split ones, which the combine kernel
-//   merges as soon as each virtual batch's splits are announced.
+//   tensor memory only when the running maximum grows by more than 2^8.  Logits, maxima, sums and O
+//   are float32; the weights alone are rounded to the cache's 16-bit type before P V, because the
+//   tensor cores take both operands in one type (float32 weights would need a second product for
+//   what the rounding drops: twice the P V work).  Each weight is off by half a step of the type at most, the
+//   sums are of the unrounded ones.  Relative error against 64 bits, all elements: 1.9e-3 to 2.2e-3
+//   (bfloat16) and 2.4e-4 (float16), where float32 weights leave 1.7e-3 and 2.1e-4: the output's own rounding.
+// * Epilogue: the softmax warps drain O 64 columns at a time from tensor memory through registers
+//   straight to global memory: 16-bit O for unsplit chunks, fp32 partials and LSEs for split
+//   ones, which the combine kernel merges as soon as each virtual batch's splits are announced.
 // * The metadata, split-KV and combine kernels are launched with programmatic launch
 //   overlap.
 // * "FP8 with scale" cache (the kFp8 instantiation, 512 threads): the K producer bulk-copies
@@ -1934,8 +1938,8 @@ __device__ __forceinline__ void dequantize16(const uint4 raw, const float s, uin
 
 // The pages of every run with tokens, dequantized once into scratch pages of 576 bfloat16 columns (page j of
 // run b is scratch page b * max_blocks + j) with their block table; reads[b]: the rows of run b that its
-// groups read.  Memory bound: 1.8 KB per row.  One block per page: a warp takes 8 rows, lane l the latent columns [16 l, 16 l + 16) and position
-// columns 2 l, 2 l + 1 of each, four rows in flight.
+// groups read.  Memory bound: 1.8 KB per row.  One block per page: a warp takes 8 rows, lane l the latent
+// columns [16 l, 16 l + 16) and position columns 2 l, 2 l + 1 of each, four rows in flight.
 constexpr int kDequantThreads = 256;
 constexpr int kRow16 = 576 * 2;
 
@@ -2080,11 +2084,12 @@ static size_t metadata_smem_bytes(int nv, int num_parts)
     return static_cast<size_t>(nv) * (8 + 4 + 4) + static_cast<size_t>(num_parts) * 8 + 16;
 }
 
-// The schedule of ragged runs: one CTA (256 threads up to 512 groups: its barriers cost less; else 1024).  The group table is built in tiles of
-// one group per thread (its run found by binary search in the runs' first groups), with the cost
-// prefix carried from tile to tile; then one thread per partition, as above.  Latency bound: once
-// per step, for every layer; starts and lengths are read once, into shared memory (up to 4,096 runs).  C: the prefix sums, in shared memory where they fit (a partition's
-// binary searches then take about 0.1 us instead of several), else behind the table.
+// The schedule of ragged runs: one CTA (256 threads up to 512 groups: its barriers cost less; else 1024).
+// The group table is built in tiles of one group per thread (its run found by binary search in the runs'
+// first groups), with the cost prefix carried from tile to tile; then one thread per partition, as above.
+// Latency bound: once per step, for every layer; starts and lengths are read once, into shared memory (up
+// to 4,096 runs).  C: the prefix sums, in shared memory where they fit (a partition's binary searches then
+// take about 0.1 us instead of several), else behind the table.
 // Runs that are not an ascending split of the tokens give an empty schedule whose md rows carry an
 // error (field 5), which the decode records.  Behind the table and the prefix sums: the rows that each run's groups
 // read (none for a run without tokens, whose length and pages may be stale).
@@ -2439,11 +2444,12 @@ static mla_status check_varlen(int batch, int total_q, int h_q, int h_kv, int nu
     return MLA_OK;
 }
 
-// Whether a ragged call over an FP8 cache dequantizes its pages first.  A page costs a group of 128 query
-// rows 1.57 us of a partition when its rows are dequantized on the way and 1.0 us when they are 16-bit
-// already (pieces of 8 prompts, 64 heads, 1.4k to 8k cached rows: 1003 us against 681 us), and dequantizing
-// it costs 19 ns of the whole GPU: worth it from 2.4 groups per run on.  Scratch is one 16-bit page per
-// block-table entry; calls that would need more than 8 GiB read the FP8 rows directly.
+// Whether a ragged call over an FP8 cache dequantizes its pages first: from three groups of 128 query rows per
+// run on (the call's average).  Dequantized first against at every read, caches flushed, 64 heads over 1k to 8k
+// cached rows: 32 runs of 3 groups 182 and 171 us, of 4 groups 215 and 218, of 6 groups 279 and 306, of 8
+// groups 338 and 399; 8 pieces of 50 to 130 groups 637 and 941; 60 decodes beside 2 pieces of 240 tokens
+// (128 heads, 8.7 groups per run) 547 and 654, over 16k to 32k rows 3625 and 4346.  Scratch is one 16-bit page
+// per block-table entry; calls that would need more than 8 GiB read the FP8 rows directly.
 static bool varlen_dequantizes(int batch, int total_q, int h_q)
 {
     return static_cast<long long>(total_q) * h_q >= 3ll * kRowsPerGroup * batch;
