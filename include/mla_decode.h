@@ -158,8 +158,9 @@ MLA_API mla_status mla_get_metadata_host(const int32_t* cache_seqlens, int batch
  *
  * Device errors.  MLA_ERR_DEVICE_CHECK: requests whose lengths and block-table
  * entries are in order get their results, in this call too; what the others get
- * is unspecified.  MLA_ERR_TIMEOUT: rows of the clusters whose wait gave up are
- * not written, all others are.
+ * is unspecified.  MLA_ERR_TIMEOUT: the rows that a cluster whose wait gave up
+ * had still to do are unspecified (where they were split, not written); all
+ * others are right.
  */
 #define MLA_MAX_VIRTUAL_BATCHES 16384
 MLA_API size_t mla_decode_workspace_bytes(int batch, int s_q, int h_q, int h_kv, int num_parts);

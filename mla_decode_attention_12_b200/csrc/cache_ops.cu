@@ -321,7 +321,7 @@ struct Sum2 {
 // [8 g, 8 g + 8) of 8 rows of a stage, and the phases meet in shared memory once per page.  126 MB of
 // pages: 33.1 us, 1.7 times their reads at the copy rate (19.2).  The rest is the start (lengths, table and
 // first page in turn: a step of 64 pages takes 8.7) and whole pages dealt out to 296 blocks (1712 pages:
-// five or six each, so the last round is uneven).  39.5 with one block per SM and twice the ring, whose
+// five or six each, so that the blocks end unevenly).  39.5 with one block per SM and twice the ring, whose
 // additions and page ends nothing overlaps; 35.6 with quarter pages.
 template <bool kFp16, bool kFp8>
 __global__ void __launch_bounds__(kSumThreads, 2) mla_summarize_kernel(const SummarizeParams p)
